@@ -32,7 +32,9 @@ EXPORTS = ("gs_strerror", "gs_workspace_size", "gs_fwd_state_size", "gs_project"
            "gs_render_bwd_views", "gs_sort_keys", "gs_render_fwd", "gs_render_bwd",
            "gs_sort_keys_noalloc", "gs_plan_tiles", "gs_plan_tiles_views", "gs_timing_start",
            "gs_timing_read", "gs_set_wait_limit", "gs_render_bwd_accumulate",
-           "gs_render_fwd_zero", "gs_sort_keys_plan")
+           "gs_render_fwd_zero", "gs_sort_keys_plan", "gs_qk_workspace_size", "gs_qk_norm_rope",
+           "gs_qk_norm_rope_bwd", "gs_attention_workspace_size",
+           "gs_attention_bwd_workspace_size", "gs_attention", "gs_attention_bwd", "gs_dropout")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 

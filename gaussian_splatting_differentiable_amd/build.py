@@ -14,7 +14,8 @@ LIB = os.path.join(HERE, "libgs.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.hip", "project.hip", "bin.hip", "sort.hip", "sched.hip",
-           "render_fwd.hip", "render_bwd.hip"]
+           "render_fwd.hip", "render_bwd.hip", "tokens_api.hip", "qk_norm_rope.hip",
+           "attention_fwd.hip", "attention_bwd.hip", "dropout.hip"]
 # translation units whose decisions must be reproducible bit for bit
 NO_CONTRACT = {"bin.hip", "sort.hip", "sched.hip"}
 

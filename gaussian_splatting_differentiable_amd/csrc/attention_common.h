@@ -1,0 +1,173 @@
+// Shared parts of the attention kernels: tiles in LDS, matrix operands, masks.
+//
+// Every kernel computes with v_mfma_f32_32x32x16: operand A holds 32 rows and B
+// 32 columns of 16 contraction slots, lane l the 8 slots 8 (l / 32) .. of row or
+// column l % 32; the result holds column l % 32 and, in register i, row
+// 8 (i / 4) + 4 (l / 32) + i % 4. The scores are computed with the streamed rows
+// (keys in the forward and in dQ, queries in dK and dV) as rows and the wave's
+// own rows as columns. A lane then holds scores of one own row only, so the
+// softmax needs one exchange (lanes l and l + 32), and its registers 8 k .. + 7
+// are already the B operand of the second product: contraction slots may be in
+// any order that A shares. A for that product is the transpose of a streamed
+// tile, read by ds_read_b64_tr_b16 in that order.
+#pragma once
+#include "tokens_common.h"
+
+#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T *)(p))
+
+constexpr float ATTN_LN2 = 0.6931471805599453f;
+constexpr float ATTN_LOG2E = 1.4426950408889634f;
+constexpr int KT = 64;  // streamed rows per tile
+
+template <class E>
+using frag = vec<E, 8>;
+
+__device__ __forceinline__ f32x16 mfma(frag<bf16_t> a, frag<bf16_t> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(frag<f16_t> a, frag<f16_t> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// x of lane l combined with x of lane l ^ 32.
+__device__ __forceinline__ float other_half(float x, bool max) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+  return max ? fmaxf(a, b) : a + b;
+}
+
+__device__ __forceinline__ int wave_min(int x) {
+  for (int m = 32; m; m >>= 1) x = min(x, __shfl_xor(x, m));
+  return x;
+}
+__device__ __forceinline__ int wave_max(int x) {
+  for (int m = 32; m; m >>= 1) x = max(x, __shfl_xor(x, m));
+  return x;
+}
+__device__ __forceinline__ float wave_fmax(float x) {
+  for (int m = 32; m; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+// The keys [x, y) that query `t` of batch entry b sees; (0, 0) if it sees none.
+__device__ __forceinline__ int2 row_span(const AttnK &p, int b, int t) {
+  int lo = 0, hi = p.kv_len;
+  if (p.spans) {
+    const int2 s = p.spans[(int64_t)b * p.span_stride + t];
+    lo = max(s.x, 0);
+    hi = min(s.y, hi);
+  }
+  if (p.causal) hi = min((int64_t)hi, (int64_t)t + 1 + p.kv_len - p.q_len);
+  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Workgroups are dealt to the 8 dies in turn, each with an L2 of its own: give a
+// die a run of consecutive items, which share their heads' streamed rows.
+__device__ __forceinline__ int die_order(int block, int blocks) {
+  const int per = blocks >> 3, rest = blocks & 7, die = block & 7;
+  return die * per + min(die, rest) + (block >> 3);
+}
+
+// ---- tiles in LDS: KT rows of D elements in 16-byte chunks. Chunk c of row r is
+// stored as chunk c ^ swizzle(r) of that row, so that neither the 16-byte row
+// reads of 16 consecutive rows nor the transposing reads of 4 consecutive rows
+// meet in the 64 banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int row) {
+  if (D == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);  // D == 64: two rows to the banks
+}
+
+template <int D>
+__device__ __forceinline__ int lds_at(int row, int chunk) {  // in elements
+  return row * D + ((chunk ^ swizzle<D>(row)) << 3);
+}
+
+// A streamed matrix of `rows` rows of `dim` elements, 16-byte chunks read with
+// bounds checks: rows past its end and elements past `dim` read as 0.
+template <class E>
+struct Stream {
+  const E *base;
+  int64_t ts;
+  int rows, dim;
+};
+
+// NT threads hold one tile of R rows in registers between global memory and LDS.
+template <class E, int D, int NT, int R>
+struct Staged {
+  static constexpr int N = R * (D / 8) / NT;
+  i32x4 v[N];
+
+  __device__ __forceinline__ void load(const Stream<E> &m, int row0, int tid) {
+    const int left = min(m.rows - row0, R);
+    const int64_t bytes = left > 0 ? ((int64_t)(left - 1) * m.ts + m.dim) * 2 : 0;
+    auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(m.base + (int64_t)row0 * m.ts), 0,
+                                                  (int)bytes, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int c = i * NT + tid, row = c / (D / 8), col = c % (D / 8);
+      // past `dim`: an offset out of every tile's bounds
+      const unsigned at = 8 * col < m.dim ? (unsigned)(row * (int)m.ts + 8 * col) * 2u : 0x7fffff00u;
+      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
+    }
+  }
+
+  __device__ __forceinline__ void store(E *lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int c = i * NT + tid, row = c / (D / 8), col = c % (D / 8);
+      *(i32x4 *)(lds + lds_at<D>(row, col)) = v[i];
+    }
+  }
+};
+
+// Operand of 32 rows (as rows of A or columns of B) and 16 elements from a row on.
+template <class E>
+__device__ __forceinline__ frag<E> row_operand(const E *row, int chunk, bool on) {
+  frag<E> f = (E)0.0f;
+  if (on) f = *(const frag<E> *)(row + 8 * chunk);
+  return f;
+}
+
+template <class E, int D>
+__device__ __forceinline__ frag<E> lds_rows(const E *tile, int row0, int k, int lane) {
+  return *(const frag<E> *)(tile + lds_at<D>(row0 + (lane & 31), 2 * k + (lane >> 5)));
+}
+
+// Operand A of the transpose: rows = elements 32 d .. + 31 of the tile's rows,
+// contraction = tile rows row0 .. + 15 in the order of a score register run.
+template <class E, int D>
+__device__ __forceinline__ frag<E> lds_cols(const E *tile, int row0, int d, int lane) {
+  const int r = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
+  const int e = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      LDS_PTR(i16x4, tile + lds_at<D>(r, e >> 3) + (e & 7)));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      LDS_PTR(i16x4, tile + lds_at<D>(r + 8, e >> 3) + (e & 7)));
+  return __builtin_bit_cast(frag<E>, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Registers 8 k .. + 7 of a score block as operand B.
+template <class E>
+__device__ __forceinline__ frag<E> pack8(const f32x16 &s, int k) {
+  frag<E> f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) f[i] = (E)s[8 * k + i];  // to nearest even
+  return f;
+}
+
+// Row of the streamed 32 that register i of a lane holds.
+__device__ __forceinline__ int acc_row(int i, int lane) {
+  return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+}
+
+template <class E>
+__device__ __forceinline__ float dot_row(const E *a, const E *b, int dim) {
+  float s = 0.0f;
+  for (int d = 0; d < dim; d += 8) {
+    const vec<E, 8> x = *(const vec<E, 8> *)(a + d), y = *(const vec<E, 8> *)(b + d);
+#pragma unroll
+    for (int i = 0; i < 8; i++) s = fmaf((float)x[i], (float)y[i], s);
+  }
+  return s;
+}

@@ -485,6 +485,116 @@ int32_t gs_timing_read(int32_t which, float *ms, int32_t cap);
  * every device and thread of the process. */
 int32_t gs_set_wait_limit(int32_t probes);
 
+/* ------------------------------------------------------------ token operators
+ * For models that predict Gaussians from the tokens of image patches and train
+ * through the rasterizer: the norm and rotation of queries and keys, attention
+ * with its gradient, and dropout. Not on the pages; written from their formulas.
+ * The conventions above hold (device pointers owned by the caller, nothing
+ * allocated, work only enqueued on `stream`, nothing done after an error), but
+ * there is no status word: every error is synchronous. Tensors may be 16-bit;
+ * all sums, statistics and generated words are 32-bit. No call uses atomics, so
+ * equal inputs give equal bits.
+ *
+ * gs_tokens: a [batch][token][head][dim] tensor by its element strides; the
+ * elements of a head are contiguous. `data` and every stride in use (that of an
+ * extent above 1) are multiples of 16 bytes and not negative; inputs may repeat
+ * rows (stride 0), outputs may not overlap; token strides are below 2^23
+ * elements (GS_ERR_UNSUPPORTED). A tensor without elements may be NULL. */
+typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
+
+typedef struct {
+  void *data;
+  int64_t batch_stride, token_stride, head_stride;
+} gs_tokens;
+
+/* Norm of queries and keys for each head, and the rotation by position:
+ *   r = 1 / sqrt(mean_d x_d^2 + eps); z = x r w; out = R(position) z.
+ * R turns pair i of the first rot_dim elements by its angle: (z_i, z_{i +
+ * rot_dim/2}) or, with neighbours = 1, (z_{2i}, z_{2i+1}) -> (a c - b s,
+ * a s + b c); the other elements stay.
+ *   dim: a multiple of 8 up to 256, rot_dim a multiple of 8 up to dim (0: no
+ *     rotation); other sizes GS_ERR_UNSUPPORTED. dtype: any gs_dtype.
+ *   q_heads or k_heads may be 0 (queries or keys alone).
+ *   q_weight, k_weight [dim] float or NULL (all ones), 16-byte aligned.
+ *   cos_sin [n_positions][rot_dim] float, 16-byte aligned: the rot_dim/2 cosines,
+ *     then the sines of each position's angles (for image patches the caller's
+ *     table may mix rows, columns and views).
+ *   positions: int32, entry b * positions_stride + t is token t's row of the
+ *     table (stride 0: one list for the batch), or NULL: row t. A position
+ *     outside the table turns into NaN, in the backward too.
+ *   q_out, k_out <- may be the inputs themselves (same strides).
+ * Backward: from the gradients of q_out and k_out, those of q, k and, where not
+ * NULL, of the weights ([dim] float, summed over batch, tokens and heads in an
+ * order fixed by the sizes; both NULL: no workspace needed). The gradients of q
+ * and k may be written over those of q_out and k_out. */
+typedef struct {
+  int32_t batch, tokens, q_heads, k_heads, dim, dtype;
+  int32_t rot_dim, neighbours, n_positions;
+  float eps;
+  int64_t positions_stride;
+} gs_qk_shape;
+
+size_t gs_qk_workspace_size(const gs_qk_shape *shape);
+int32_t gs_qk_norm_rope(const gs_qk_shape *shape, const gs_tokens *q, const gs_tokens *k,
+                        const float *q_weight, const float *k_weight, const float *cos_sin,
+                        const int32_t *positions, const gs_tokens *q_out, const gs_tokens *k_out,
+                        void *stream);
+int32_t gs_qk_norm_rope_bwd(const gs_qk_shape *shape, const gs_tokens *dL_dq_out,
+                            const gs_tokens *dL_dk_out, const gs_tokens *q, const gs_tokens *k,
+                            const float *q_weight, const float *k_weight, const float *cos_sin,
+                            const int32_t *positions, const gs_tokens *dL_dq,
+                            const gs_tokens *dL_dk, float *dL_dq_weight, float *dL_dk_weight,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Attention: s_ij = scale q_i . k_j over the keys j that query i sees,
+ * lse_i = log sum_j exp s_ij, o_i = sum_j exp(s_ij - lse_i) v_j. Query heads
+ * h * (q_heads / kv_heads) .. share key head h.
+ *   dtype GS_BF16 or GS_F16 (GS_F32: GS_ERR_UNSUPPORTED); dim a multiple of 8
+ *     up to 128; scale > 0; up to 2^30 tokens.
+ *   spans: int32 pairs [lo, hi) of the keys a query sees, pair b * spans_stride +
+ *     t for query t (stride 0: one list for the batch), 8-byte aligned, or NULL:
+ *     all keys. Parts outside [0, kv_tokens) are cut off. Spans express padding,
+ *     several sequences packed into one, windows and views in order.
+ *   causal = 1: query t also sees no key above t + kv_tokens - q_tokens.
+ *   A query that sees no key gets o = 0, lse = -inf and zero gradients. What a
+ *     masked key or query holds (NaN and infinity included) reaches no result.
+ *   o, lse [batch][q_heads][q_tokens] float <- written.
+ *   workspace: gs_attention_workspace_size bytes, 256-byte aligned (0: NULL);
+ *     it depends on the sizes only: few rows over many keys are computed in
+ *     parts, which are joined in 32 bits.
+ * Backward: the gradients of q, k and v from that of o, with o and lse as the
+ * forward left them (the probabilities are computed again; lse passes no
+ * gradient). The workspace is gs_attention_bwd_workspace_size bytes. */
+typedef struct {
+  int32_t batch, q_heads, kv_heads, q_tokens, kv_tokens, dim, dtype, causal;
+  float scale;
+  int64_t spans_stride;
+} gs_attn_shape;
+
+size_t gs_attention_workspace_size(const gs_attn_shape *shape);
+size_t gs_attention_bwd_workspace_size(const gs_attn_shape *shape);
+int32_t gs_attention(const gs_attn_shape *shape, const gs_tokens *q, const gs_tokens *k,
+                     const gs_tokens *v, const int32_t *spans, const gs_tokens *o, float *lse,
+                     void *workspace, size_t workspace_bytes, void *stream);
+int32_t gs_attention_bwd(const gs_attn_shape *shape, const gs_tokens *dL_do, const gs_tokens *q,
+                         const gs_tokens *k, const gs_tokens *v, const int32_t *spans,
+                         const gs_tokens *o, const float *lse, const gs_tokens *dL_dq,
+                         const gs_tokens *dL_dk, const gs_tokens *dL_dv, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Dropout with a mask that is generated, never stored:
+ *   y = residual + (word(i) >= p 2^32 ? x / (1 - p) : 0), residual NULL: 0.
+ * word(i) is word i % 4 of the Philox 4x32 block (10 rounds; J. Salmon et al.,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) at counter offset + i / 4
+ * under the key `seed`; i is the element's index r cols + c, or with per_row = 1
+ * the row r (whole tokens or Gaussians). The gradient with respect to x is the
+ * same call on dL/dy without a residual. A call uses ceil(count / 4) counters.
+ *   x, residual, y [rows][cols] by their row strides (elements), any alignment
+ *     of the type; y may be x or residual (same stride). 0 <= p < 1. */
+int32_t gs_dropout(int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t x_stride,
+                   const void *residual, int64_t residual_stride, void *y, int64_t y_stride,
+                   double p, uint64_t seed, uint64_t offset, int32_t per_row, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
