@@ -223,22 +223,50 @@ __device__ __forceinline__ uint32_t store_rows(const f32x16 (&acc)[D / 32], floa
   return skip;
 }
 
+// The same into one part's 32-bit sums, which k_attn_sum adds and looks over.
+template <int D>
+__device__ __forceinline__ void store_part(const f32x16 (&acc)[D / 32], float by, float *row,
+                                           bool on, int dim, int lane) {
+#pragma unroll
+  for (int d = 0; d < D / 32; d++)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int e = 32 * d + acc_row(i, lane);
+      const f32x16 x = acc[d];
+      if (on && e < dim) *(f32x4 *)(row + e) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]} * by;
+    }
+}
+
 // ------------------------------------------------------------ dK and dV
-// A block of four waves owns 128 keys of one key head (32 a wave, K and V in
-// registers) and streams the queries that see them, head after head of those that
-// share the key head, in tiles of 64.
+// A block owns 128 keys of one key head, a wave 32 of them (K and V as operands in
+// registers), and streams the queries that see them in tiles of 64, head after
+// head of those that share the key head. Where there are too few such blocks, or
+// masks make them uneven, a block takes one of kv_parts equal runs of those tiles,
+// and k_attn_sum adds the parts' 32-bit sums.
+//
+// The steps of one 32 x 32 block are spread over two turns of the loop, so that
+// the vector unit and the matrix unit work at the same time in the one wave that
+// a SIMD has room for (D = 128: K, V, dK, dV and two sets of operands take most
+// of the 512 registers): a turn computes the scores of block s, then its
+// probabilities while the matrix unit adds block s - 1 to dK and dV and the rows
+// of block s + 1 arrive from LDS. -lse / scale and -D_i are the accumulators'
+// starting values.
 template <class E, int D>
 __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, int tiles,
                                                                        int q_tiles) {
-  __shared__ __attribute__((aligned(16))) E lds[2][2][KT * D];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][KT];
-  __shared__ __attribute__((aligned(16))) int2 spans[2][KT];
+  // Objects of their own, and turns of the loop that name theirs: the compiler then
+  // sees that reads of one do not wait for copies into another.
+  using Buf = E[2][KT * D];
+  __shared__ __attribute__((aligned(16))) Buf b0, b1, b2;
+  __shared__ __attribute__((aligned(16))) float stat[3][2][KT];
+  __shared__ __attribute__((aligned(16))) int2 spans[3][KT];
   __shared__ uint64_t active[WALK / 64], partial[WALK / 64];
   __shared__ float tops[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = die_order(blockIdx.x, gridDim.x);
-  const int bh = item / tiles, b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
-  const int key0 = (item - bh * tiles) * 128, mine0 = key0 + 32 * wave;
+  const int piece = item % p.kv_parts, whole = item / p.kv_parts;
+  const int bh = whole / tiles, b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
+  const int key0 = (whole - bh * tiles) * 128, mine0 = key0 + 32 * wave;
   const int key = mine0 + (lane & 31);
   const bool on = key < p.kv_len;
 
@@ -271,10 +299,11 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, i
   for (int d = 0; d < D / 32; d++) dk[d] = dv[d] = 0.0f;
 
   for (int walk0 = 0; walk0 < q_tiles; walk0 += WALK) {
-    // Which of the next WALK query tiles see a key of this block, and which of
-    // them not all of its keys with all of their rows.
+    // Which of the next WALK tiles see a key of this block, and which of them not
+    // all of its keys with all of their rows.
+    const int words = (min(q_tiles - walk0, WALK) + 63) >> 6;
     __syncthreads();
-    for (int i = tid; i < WALK; i += 256) {
+    for (int i = tid; i < words * 64; i += 256) {
       const int qt = walk0 + i;
       bool act = qt < q_tiles, part = false;
       if (act && p.tile_spans) {
@@ -289,8 +318,17 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, i
       }
     }
     __syncthreads();
+    // This block's run of the (head, tile) pairs: `left` pairs from tile qt of
+    // head `head` on.
+    int count = 0;
+    for (int w = 0; w < words; w++) count += __builtin_popcountll(active[w]);
+    count = __builtin_amdgcn_readfirstlane(count);
+    const int64_t pairs = (int64_t)count * p.share;
+    const int64_t from = pairs * piece / p.kv_parts;
+    int left = (int)(pairs * (piece + 1) / p.kv_parts - from);
+    if (left == 0) continue;
     auto next = [&](int from) {  // the first active tile from `from` on, or -1
-      for (int w = from >> 6; w < WALK / 64; w++) {
+      for (int w = from >> 6; w < words; w++) {
         uint64_t m = active[w];
         if (w == from >> 6) m &= ~0ull << (from & 63);
         if (m) return __builtin_amdgcn_readfirstlane((w << 6) + __builtin_ctzll(m));
@@ -298,101 +336,186 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, i
       return -1;
     };
     const int first = next(0);
-    if (first < 0) continue;
+    int head = kvh * p.share + (int)(from / count), qt = first;
+    if (from % count) {  // the active tile number from % count
+      int skip = (int)(from % count), w = 0;
+      uint64_t m = active[0];
+      for (; skip >= __builtin_popcountll(m); m = active[++w]) skip -= __builtin_popcountll(m);
+      for (; skip > 0; skip--) m &= m - 1;
+      qt = __builtin_amdgcn_readfirstlane((w << 6) + __builtin_ctzll(m));
+    }
 
-    Staged<E, D, 256, KT> sq, sg;
     float lse = 0.0f, delta = 0.0f;
     int2 span = make_int2(0, 0);
-    auto load = [&](int head, int qt) {
+    int row = 0;
+    using Tile = Copy<E, D, 256, KT>;
+    auto load = [&](int head, int qt, Buf &to) {  // the row values wait in registers for put()
       const int t0 = (walk0 + qt) * KT;
-      sq.load({tok_row<E>(p.q, b, 0, head), p.q.ts, p.q_len, p.dim}, t0, tid);
-      sg.load({tok_row<E>(p.d_o, b, 0, head), p.d_o.ts, p.q_len, p.dim}, t0, tid);
+      Tile::issue({tok_row<E>(p.q, b, 0, head), p.q.ts, p.q_len, p.dim}, t0, to[0], tid);
+      Tile::issue({tok_row<E>(p.d_o, b, 0, head), p.d_o.ts, p.q_len, p.dim}, t0, to[1], tid);
       if (tid < KT) {
-        const int t = t0 + tid;
+        row = t0 + tid;
         lse = -INFINITY;
         delta = 0.0f;
         span = make_int2(0, 0);
-        if (t < p.q_len) {
-          const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
+        if (row < p.q_len) {
+          const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + row;
           lse = p.lse[at];
           delta = p.delta[at];
-          if (p.tile_spans) span = row_span(p, b, t);
+          if (p.tile_spans) span = raw_span(p, b, row);
         }
       }
     };
     auto put = [&](int at) {
-      sq.store(lds[at][0], tid);
-      sg.store(lds[at][1], tid);
       if (tid < KT) {
         // a row that sees nothing, or is past the end: p = 2^-inf = 0
-        stat[at][0][tid] = lse == -INFINITY ? INFINITY
-                                            : lse * ATTN_LOG2E - (is_half<E> ? 15.0f : 0.0f);
-        stat[at][1][tid] = delta;
-        spans[at][tid] = span;
+        stat[at][0][tid] = lse == -INFINITY
+                                    ? -INFINITY
+                                    : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
+        stat[at][1][tid] = -delta;
+        spans[at][tid] = cut_span(p, row, span);
       }
     };
-    int head = kvh * p.share, qt = first, at = 0;
-    const int heads = head + p.share;
-    load(head, qt);
-    put(0);
-    __syncthreads();
-    while (head < heads) {
-      int nqt = next(qt + 1), nhead = head;
-      if (nqt < 0) {
-        nqt = first;
-        nhead++;
+    auto after = [&](int &h, int &t) {  // the tile after tile t of head h
+      t = next(t + 1);
+      if (t < 0) {
+        t = first;
+        h++;
       }
-      if (nhead < heads) load(nhead, nqt);
+    };
+    frag<E> rq[D / 16], rg[D / 16], cq[2][D / 32], cg[2][D / 32], pw[2], pd[2];
+    auto rows = [&](Buf &of, int row0) {
+#pragma unroll
+      for (int k = 0; k < D / 16; k++) {
+        rq[k] = lds_rows<E, D>(of[0], row0, k, lane);
+        rg[k] = lds_rows<E, D>(of[1], row0, k, lane);
+      }
+    };
+    auto add = [&]() {  // the last block into dK and dV
+#pragma unroll
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int d = 0; d < D / 32; d++) {
+          dv[d] = mfma(cg[k][d], pw[k], dv[d]);
+          dk[d] = mfma(cq[k][d], pd[k], dk[d]);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      pw[k] = pd[k] = (E)0.0f;
+#pragma unroll
+      for (int d = 0; d < D / 32; d++) cq[k][d] = cg[k][d] = (E)0.0f;
+    }
+    auto sync = [&]() {  // the tile put last is there
+      copied<0>();
+      __syncthreads();
+    };
+
+    int nhead = head, nqt = qt;
+    load(head, qt, b0);
+    put(0);
+    sync();
+    after(nhead, nqt);
+    if (left > 1) load(nhead, nqt, b1);
+    rows(b0, 0);
+    // One tile, in buffer `at`; the next one goes to buffer `to`, the one after it
+    // to `then`.
+    auto turn = [&](Buf &here, Buf &there, Buf &then, int at, int to) {
       const bool part = partial[qt >> 6] >> (qt & 63) & 1;
-      const E *qs = lds[at][0], *gs = lds[at][1];
 #pragma unroll
       for (int s = 0; s < KT / 32; s++) {
-        f32x16 w = 0.0f, ds = 0.0f;
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-          w = mfma(lds_rows<E, D>(qs, 32 * s, k, lane), kf[k], w);
-          ds = mfma(lds_rows<E, D>(gs, 32 * s, k, lane), vf[k], ds);
-        }
+        const bool last = s == KT / 32 - 1;
+        f32x16 w, ds;
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const int r = 32 * s + acc_row(i, lane);
-          const f32x4 l4 = *(const f32x4 *)&stat[at][0][r], d4 = *(const f32x4 *)&stat[at][1][r];
+          const f32x4 l4 = *(const f32x4 *)&stat[at][0][r];
+          const f32x4 d4 = *(const f32x4 *)&stat[at][1][r];
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            w[i + c] = __builtin_amdgcn_exp2f(fmaf(w[i + c], p.scale_log2, -l4[c]));
-            ds[i + c] = w[i + c] * (ds[i + c] - d4[c]);
-            if (is_half<E>) ds[i + c] *= ds_by;
+            w[i + c] = l4[c];
+            ds[i + c] = d4[c];
           }
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; k++) {
+          w = mfma(rq[k], kf[k], w);
+          ds = mfma(rg[k], vf[k], ds);
         }
         if (part) {
 #pragma unroll
           for (int i = 0; i < 16; i++) {
             const int2 r = spans[at][32 * s + acc_row(i, lane)];
-            if ((unsigned)(key - r.x) >= (unsigned)(r.y - r.x)) w[i] = ds[i] = 0.0f;
+            if ((unsigned)(key - r.x) >= (unsigned)(r.y - r.x)) {
+              w[i] = -INFINITY;
+              ds[i] = 0.0f;
+            }
           }
         }
+        if (last) {
+          // The next tile's values are put and its copies awaited; the one after it
+          // is sent for, into the buffer whose last reads came before this barrier in
+          // every wave.
+          if (left > 1) put(to);
+          sync();
+          qt = nqt;
+          left--;
+          after(nhead, nqt);
+          if (left > 1) load(nhead, nqt, then);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        add();
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          w[i] = __builtin_amdgcn_exp2f(w[i] * p.scale_log2);
+          ds[i] *= w[i];
+          if (is_half<E>) ds[i] *= ds_by;
+        }
+        // past the last tile these are reads of what the buffer holds, for nothing
+        rows(last ? there : here, last ? 0 : 32 * (s + 1));
+        // In order: a matrix instruction, its share of the vector work and of the reads.
+        // A wave issues in order, and a matrix instruction holds it while the unit is
+        // busy: vector work placed behind all of them would wait for all of them.
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // matrix
+          __builtin_amdgcn_sched_group_barrier(0x002, 3 * 128 / D, 0);    // vector
+          __builtin_amdgcn_sched_group_barrier(0x400, 128 / D, 0);        // exp
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);              // LDS read
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-          const frag<E> pw = pack8<E>(w, k), pd = pack8<E>(ds, k);
+          pw[k] = pack8<E>(w, k);
+          pd[k] = pack8<E>(ds, k);
 #pragma unroll
           for (int d = 0; d < D / 32; d++) {
-            dv[d] = mfma(lds_cols<E, D>(gs, 32 * s + 16 * k, d, lane), pw, dv[d]);
-            dk[d] = mfma(lds_cols<E, D>(qs, 32 * s + 16 * k, d, lane), pd, dk[d]);
+            cg[k][d] = lds_cols<E, D>(here[1], 32 * s + 16 * k, d, lane);
+            cq[k][d] = lds_cols<E, D>(here[0], 32 * s + 16 * k, d, lane);
           }
         }
       }
-      if (nhead < heads) put(at ^ 1);
-      __syncthreads();
-      head = nhead;
-      qt = nqt;
-      at ^= 1;
+    };
+    while (left > 0) {
+      turn(b0, b1, b2, 0, 1);
+      if (left > 0) turn(b1, b2, b0, 1, 2);
+      if (left > 0) turn(b2, b0, b1, 2, 0);
     }
+    add();
   }
 
-  uint32_t again = store_rows<E, D>(dk, is_half<E> ? ldexpf(p.scale, -e) : p.scale,
-                                    tok_row<E>(p.dk, b, key, kvh), on, p.dim, lane, 0);
-  again |= store_rows<E, D>(dv, is_half<E> ? 0x1p-15f : 1.0f, tok_row<E>(p.dv, b, key, kvh), on,
-                            p.dim, lane, again);
+  const float by_k = is_half<E> ? ldexpf(p.scale, -e) : p.scale, by_v = is_half<E> ? 0x1p-15f : 1.0f;
+  if (p.kv_parts > 1) {
+    const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;
+    const int64_t at = (piece * rows + (int64_t)bh * p.kv_len + key) * p.dim;
+    store_part<D>(dk, by_k, p.part_k + at, on, p.dim, lane);
+    store_part<D>(dv, by_v, p.part_v + at, on, p.dim, lane);
+    return;
+  }
+  uint32_t again =
+      store_rows<E, D>(dk, by_k, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane, 0);
+  again |= store_rows<E, D>(dv, by_v, tok_row<E>(p.dv, b, on ? key : 0, kvh), on, p.dim, lane,
+                            again);
   if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
   while (again) {
     const int r = __builtin_ctz(again);
@@ -402,17 +525,20 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, i
 }
 
 // ------------------------------------------------------------ dQ
-// The forward's walk with a second score product and without a running maximum.
+// The forward's walk with a second score product and without a running maximum; a
+// block takes one of q_parts runs of its key tiles, as above.
 template <class E, int D, int NQ>
 __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK p, int tiles,
                                                                             int kv_tiles) {
-  __shared__ __attribute__((aligned(16))) E lds[2][2][KT * D];
+  using Buf = E[2][KT * D];
+  __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
   __shared__ float tops[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = die_order(blockIdx.x, gridDim.x);
-  const int bh = item / tiles, b = bh / p.q_heads, head = bh - b * p.q_heads;
-  const int tile = p.causal ? tiles - 1 - (item - bh * tiles) : item - bh * tiles;
+  const int piece = item % p.q_parts, whole = item / p.q_parts;
+  const int2 at = block_item(p, whole, p.batch * p.q_heads, tiles);
+  const int bh = at.x, tile = at.y, b = bh / p.q_heads, head = bh - b * p.q_heads;
   const int kvh = head / p.share, row0 = tile * 128 * NQ + wave * 32 * NQ + (lane & 31);
 
   float v_top = 0.0f;
@@ -469,6 +595,11 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
   }
   first = __builtin_amdgcn_readfirstlane(first < end ? first / KT : 0);
   end = __builtin_amdgcn_readfirstlane((end + KT - 1) / KT);
+  if (p.q_parts > 1) {
+    const int n = end > first ? end - first : 0;
+    end = first + (int)((int64_t)n * (piece + 1) / p.q_parts);
+    first += (int)((int64_t)n * piece / p.q_parts);
+  }
 
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
@@ -477,83 +608,127 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
   for (int n = 0; n < NQ; n++)
 #pragma unroll
     for (int d = 0; d < D / 32; d++) dq[n][d] = 0.0f;
-  Staged<E, D, 256, KT> sk, sv;
+  using Tile = Copy<E, D, 256, KT>;
   if (first < end) {
-    sk.load(ks, first * KT, tid);
-    sv.load(vs, first * KT, tid);
-    sk.store(lds[0][0], tid);
-    sv.store(lds[0][1], tid);
+    Tile::issue(ks, first * KT, b0[0], tid);
+    Tile::issue(vs, first * KT, b0[1], tid);
   }
-  __syncthreads();
-  for (int j = first; j < end; j++) {
-    const int at = (j - first) & 1;
+  auto turn = [&](int j, Buf &here, Buf &there) {
+    block_copied();  // tile j is there, and nobody reads the other one any more
     if (j + 1 < end) {
-      sk.load(ks, (j + 1) * KT, tid);
-      sv.load(vs, (j + 1) * KT, tid);
+      Tile::issue(ks, (j + 1) * KT, there[0], tid);
+      Tile::issue(vs, (j + 1) * KT, there[1], tid);
     }
     const int key0 = j * KT;
-    if (key0 < hi && key0 + KT > lo) {
-      const bool full = key0 >= in_lo && key0 + KT <= in_hi;
-      const E *kt = lds[at][0], *vt = lds[at][1];
+    if (key0 >= hi || key0 + KT <= lo) return;
+    const bool full = key0 >= in_lo && key0 + KT <= in_hi;
+    const E *kt = here[0], *vt = here[1];
 #pragma unroll
-      for (int s = 0; s < KT / 32; s++) {
-        f32x16 w[NQ], ds[NQ];
+    for (int s = 0; s < KT / 32; s++) {
+      f32x16 w[NQ], ds[NQ];
+      frag<E> a[D / 16], c[D / 16];
 #pragma unroll
-        for (int n = 0; n < NQ; n++) w[n] = ds[n] = 0.0f;
+      for (int k = 0; k < D / 16; k++) a[k] = lds_rows<E, D>(kt, 32 * s, k, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-          const frag<E> a = lds_rows<E, D>(kt, 32 * s, k, lane), c = lds_rows<E, D>(vt, 32 * s, k, lane);
+      for (int k = 0; k < D / 16; k++) c[k] = lds_rows<E, D>(vt, 32 * s, k, lane);
 #pragma unroll
-          for (int n = 0; n < NQ; n++) {
-            w[n] = mfma(a, q[n][k], w[n]);
-            ds[n] = mfma(c, g[n][k], ds[n]);
-          }
-        }
+      for (int n = 0; n < NQ; n++) {
+        w[n] = ds[n] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NQ; n++) {
+        for (int k = 0; k < D / 16; k++) w[n] = mfma(a[k], q[n][k], w[n]);
 #pragma unroll
-          for (int i = 0; i < 16; i++)
-            ds[n][i] = __builtin_amdgcn_exp2f(fmaf(w[n][i], p.scale_log2, -lse[n])) *
-                       (ds[n][i] - delta[n]);
-          if (!full) {
+        for (int k = 0; k < D / 16; k++) ds[n] = mfma(c[k], g[n][k], ds[n]);
+      }
+      frag<E> cols[2][D / 32];  // on their way while the vector unit works
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              const int key = key0 + 32 * s + acc_row(i, lane);
-              if ((unsigned)(key - span[n].x) >= (unsigned)(span[n].y - span[n].x)) ds[n][i] = 0.0f;
-            }
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int d = 0; d < D / 32; d++) cols[k][d] = lds_cols<E, D>(kt, 32 * s + 16 * k, d, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NQ; n++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+          ds[n][i] = __builtin_amdgcn_exp2f(fmaf(w[n][i], p.scale_log2, -lse[n])) *
+                     (ds[n][i] - delta[n]);
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int key = key0 + 32 * s + acc_row(i, lane);
+            if ((unsigned)(key - span[n].x) >= (unsigned)(span[n].y - span[n].x)) ds[n][i] = 0.0f;
           }
         }
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-          frag<E> pd[NQ];
+          const frag<E> pd = pack8<E>(ds[n], k);
 #pragma unroll
-          for (int n = 0; n < NQ; n++) pd[n] = pack8<E>(ds[n], k);
-#pragma unroll
-          for (int d = 0; d < D / 32; d++) {
-            const frag<E> a = lds_cols<E, D>(kt, 32 * s + 16 * k, d, lane);
-#pragma unroll
-            for (int n = 0; n < NQ; n++) dq[n][d] = mfma(a, pd[n], dq[n][d]);
-          }
+          for (int d = 0; d < D / 32; d++) dq[n][d] = mfma(cols[k][d], pd, dq[n][d]);
         }
       }
     }
-    if (j + 1 < end) {
-      sk.store(lds[at ^ 1][0], tid);
-      sv.store(lds[at ^ 1][1], tid);
-    }
-    __syncthreads();
+  };
+  for (int j = first; j < end; j += 2) {
+    turn(j, b0, b1);
+    if (j + 1 < end) turn(j + 1, b1, b0);
   }
 #pragma unroll
   for (int n = 0; n < NQ; n++) {
     const int t = row0 + 32 * n;
     const bool on = t < p.q_len;
-    uint32_t again = store_rows<E, D>(dq[n], is_half<E> ? ldexpf(p.scale, -e[n]) : p.scale,
-                                      tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim, lane, 0);
+    const float by = is_half<E> ? ldexpf(p.scale, -e[n]) : p.scale;
+    if (p.q_parts > 1) {
+      const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
+      store_part<D>(dq[n], by, p.part_q + (piece * rows + (int64_t)bh * p.q_len + t) * p.dim, on,
+                    p.dim, lane);
+      continue;
+    }
+    uint32_t again = store_rows<E, D>(dq[n], by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim,
+                                      lane, 0);
     while (again) {
       const int r = __builtin_ctz(again);
       again &= again - 1;
       redo_query<E>(p, b, head, tile * 128 * NQ + wave * 32 * NQ + 32 * n + r, lane);
     }
+  }
+}
+
+// ------------------------------------------------------------ the parts' sums
+// 32 lanes a row, in the order of the parts: rows of dQ (KEYS 0), or of dK and dV.
+template <class E, bool KEYS>
+__global__ __launch_bounds__(256) void k_attn_sum(AttnK p) {
+  const int lane = threadIdx.x & 63, e = 4 * (lane & 31);
+  const int len = KEYS ? p.kv_len : p.q_len, heads = KEYS ? p.kv_heads : p.q_heads;
+  const int parts = KEYS ? p.kv_parts : p.q_parts;
+  const int64_t rows = (int64_t)p.batch * heads * len;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const bool on = row < rows && e < p.dim;
+  const int64_t bh = (on ? row : 0) / len;
+  const int t = (int)((on ? row : 0) - bh * len), b = (int)(bh / heads);
+  const int head = (int)(bh - (int64_t)b * heads);
+  f32x4 x = 0.0f, y = 0.0f;
+  if (on) {
+    const float *px = (KEYS ? p.part_k : p.part_q) + row * p.dim + e;
+    const float *py = p.part_v + row * p.dim + e;
+#pragma unroll 4
+    for (int i = 0; i < parts; i++) {
+      x += *(const f32x4 *)(px + i * rows * p.dim);
+      if (KEYS) y += *(const f32x4 *)(py + i * rows * p.dim);
+    }
+    store4(tok_row<E>(KEYS ? p.dk : p.dq, b, t, head) + e, x);
+    if (KEYS) store4(tok_row<E>(p.dv, b, t, head) + e, y);
+  }
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 4; i++) nan |= x[i] != x[i] || y[i] != y[i];
+  const uint64_t bits = __builtin_amdgcn_ballot_w64(nan);
+  if (!bits) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
+  for (int h = 0; h < 2; h++) {
+    if (!(uint32_t)(bits >> (32 * h))) continue;
+    const int hb = __shfl(b, 32 * h), hh = __shfl(head, 32 * h), ht = __shfl(t, 32 * h);
+    if (KEYS) redo_key<E>(p, hb, hh, ht, lane);
+    else redo_query<E>(p, hb, hh, ht, lane);
   }
 }
 
@@ -565,14 +740,48 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int k_tiles = (p.kv_len + 127) / 128, tiles = (p.q_len + 127) / 128;
-  if (k_tiles) k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles, 256, 0, st>>>(p, k_tiles, q_tiles);
-  err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  if (tiles) k_attn_bwd_q<E, D, 1><<<p.batch * p.q_heads * tiles, 256, 0, st>>>(p, tiles, kv_tiles);
+  if (k_tiles) {
+    k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles * p.kv_parts, 256, 0, st>>>(p, k_tiles,
+                                                                                    q_tiles);
+    if (p.kv_parts > 1) {
+      const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;
+      k_attn_sum<E, true><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
+    }
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  if (tiles) {
+    k_attn_bwd_q<E, D, 1><<<p.batch * p.q_heads * tiles * p.q_parts, 256, 0, st>>>(p, tiles,
+                                                                                   kv_tiles);
+    if (p.q_parts > 1) {
+      const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
+      k_attn_sum<E, false><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
+    }
+  }
   return hipGetLastError();
 }
 
 }  // namespace
+
+// Parts of a block's streamed tiles: enough to have a workgroup for each of 256
+// compute units, at least two where masks make the blocks uneven and they are no
+// more than one for each, every part with four tiles or more. A part costs the
+// write and the read of its 32-bit sums.
+// Measured, q_len 2331, 8 heads of 64 (152 blocks), dK and dV with their sum: one
+// part 57 us, two 44, four 45; causal, 2 x 4096 queries, 16 heads of 128 on 4 (256
+// blocks): one 576, two 395.
+void gs_attn_bwd_plan(AttnK *p, bool masked) {
+  auto parts = [masked](int64_t blocks, int64_t tiles) {
+    int64_t n = blocks ? (256 + blocks - 1) / blocks : 1;
+    if (masked && blocks <= 256) n = n < 2 ? 2 : n;
+    n = n < tiles / 4 ? n : tiles / 4;
+    return (int)(n < 1 ? 1 : n < 16 ? n : 16);
+  };
+  p->kv_parts = parts((int64_t)p->batch * p->kv_heads * ((p->kv_len + 127) / 128),
+                      (int64_t)((p->q_len + 63) / 64) * p->share);
+  p->q_parts = parts((int64_t)p->batch * p->q_heads * ((p->q_len + 127) / 128),
+                     (p->kv_len + 63) / 64);
+}
 
 hipError_t gs_launch_attn_bwd(const AttnK &p, int dtype, hipStream_t st) {
   if (dtype == GS_BF16) return p.dim <= 64 ? launch<bf16_t, 64>(p, st) : launch<bf16_t, 128>(p, st);

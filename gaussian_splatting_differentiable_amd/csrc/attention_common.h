@@ -49,16 +49,27 @@ __device__ __forceinline__ float wave_fmax(float x) {
   return x;
 }
 
-// The keys [x, y) that query `t` of batch entry b sees; (0, 0) if it sees none.
-__device__ __forceinline__ int2 row_span(const AttnK &p, int b, int t) {
-  int lo = 0, hi = p.kv_len;
-  if (p.spans) {
-    const int2 s = p.spans[(int64_t)b * p.span_stride + t];
-    lo = max(s.x, 0);
-    hi = min(s.y, hi);
-  }
+// Orders this wave's LDS stores before its later LDS loads (and the reverse), for
+// LDS that only this wave uses.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The keys [x, y) that query `t` of batch entry b sees; (0, 0) if it sees none: the
+// span as it is stored, and cut to the keys and the causal rule.
+__device__ __forceinline__ int2 raw_span(const AttnK &p, int b, int t) {
+  return p.spans ? p.spans[(int64_t)b * p.span_stride + t] : make_int2(0, p.kv_len);
+}
+__device__ __forceinline__ int2 cut_span(const AttnK &p, int t, int2 s) {
+  const int lo = max(s.x, 0);
+  int hi = min(s.y, p.kv_len);
   if (p.causal) hi = min((int64_t)hi, (int64_t)t + 1 + p.kv_len - p.q_len);
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+__device__ __forceinline__ int2 row_span(const AttnK &p, int b, int t) {
+  return cut_span(p, t, raw_span(p, b, t));
 }
 
 // Workgroups are dealt to the 8 dies in turn, each with an L2 of its own: give a
@@ -66,6 +77,16 @@ __device__ __forceinline__ int2 row_span(const AttnK &p, int b, int t) {
 __device__ __forceinline__ int die_order(int block, int blocks) {
   const int per = blocks >> 3, rest = blocks & 7, die = block & 7;
   return die * per + min(die, rest) + (block >> 3);
+}
+
+// Head (x) and row tile (y) of an item: a head's tiles in a row, so that they share
+// its keys in their die's L2. Causal rows see more keys the later they are: there
+// the last tiles of a die's heads come first, so that the longest blocks do.
+__device__ __forceinline__ int2 block_item(const AttnK &p, int item, int heads, int tiles) {
+  if (!p.causal) return make_int2(item / tiles, item % tiles);
+  const int per = max(heads >> 3, 1), group = item / (per * tiles);
+  const int rest = item - group * per * tiles, n = min(per, heads - group * per);
+  return make_int2(group * per + rest % n, tiles - 1 - rest / n);
 }
 
 // ---- tiles in LDS: KT rows of D elements in 16-byte chunks. Chunk c of row r is
@@ -92,58 +113,70 @@ struct Stream {
   int rows, dim;
 };
 
-// NT threads hold one tile of R rows in registers between global memory and LDS.
+// NT threads copy one tile of R rows from global memory straight into LDS (no
+// registers in between): N copies of 16 bytes a thread. The copies of a wave land
+// in consecutive chunks, so the swizzle is applied to where a lane reads: lanes of
+// a row read all of its chunks, in another order. Bounds as for Stream. The data
+// is there after copied<>() in the issuing wave.
 template <class E, int D, int NT, int R>
-struct Staged {
-  static constexpr int N = R * (D / 8) / NT;
-  i32x4 v[N];
+struct Copy {
+  static constexpr int C = D / 8, N = R * C / NT;
 
-  __device__ __forceinline__ void load(const Stream<E> &m, int row0, int tid) {
+  static __device__ __forceinline__ void issue(const Stream<E> &m, int row0, E *lds, int tid) {
     const int left = min(m.rows - row0, R);
     const int64_t bytes = left > 0 ? ((int64_t)(left - 1) * m.ts + m.dim) * 2 : 0;
     auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(m.base + (int64_t)row0 * m.ts), 0,
                                                   (int)bytes, 0x00020000);
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int c = i * NT + tid, row = c / (D / 8), col = c % (D / 8);
+      const int row = i * (NT / C) + tid / C, col = (tid % C) ^ swizzle<D>(row);
       // past `dim`: an offset out of every tile's bounds
       const unsigned at = 8 * col < m.dim ? (unsigned)(row * (int)m.ts + 8 * col) * 2u : 0x7fffff00u;
-      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
-    }
-  }
-
-  __device__ __forceinline__ void store(E *lds, int tid) const {
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      const int c = i * NT + tid, row = c / (D / 8), col = c % (D / 8);
-      *(i32x4 *)(lds + lds_at<D>(row, col)) = v[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, LDS_PTR(void, lds + (i * NT + (NT > 64 ? tid & ~63 : 0)) * 8), 16, at, 0, 0, 0);
     }
   }
 };
 
-// Operand of 32 rows (as rows of A or columns of B) and 16 elements from a row on.
-template <class E>
-__device__ __forceinline__ frag<E> row_operand(const E *row, int chunk, bool on) {
-  frag<E> f = (E)0.0f;
-  if (on) f = *(const frag<E> *)(row + 8 * chunk);
-  return f;
+// Waits until at most `left` of this wave's newest memory operations are under way
+// (0: all are done), and for its LDS reads.
+template <int left>
+__device__ __forceinline__ void copied() {
+  __builtin_amdgcn_s_waitcnt((left & 15) | (left >> 4 << 14) | 0x70);
 }
 
+// Tiles that the block copied are there for all its waves.
+__device__ __forceinline__ void block_copied() {
+  copied<0>();
+  __syncthreads();
+}
+
+// Operand of 32 rows (as rows of A or columns of B) and 16 elements from a row on;
+// zero where not `on`. The load is made either way, from the row's start then, so
+// that the loads of a row are under way together and not each in a branch.
+template <class E>
+__device__ __forceinline__ frag<E> row_operand(const E *row, int chunk, bool on) {
+  const frag<E> f = *(const frag<E> *)(row + (on ? 8 * chunk : 0));
+  return on ? f : (frag<E>)(E)0.0f;
+}
+
+// row0: a multiple of 32, so that the swizzle depends on the lane alone.
 template <class E, int D>
 __device__ __forceinline__ frag<E> lds_rows(const E *tile, int row0, int k, int lane) {
-  return *(const frag<E> *)(tile + lds_at<D>(row0 + (lane & 31), 2 * k + (lane >> 5)));
+  return *(const frag<E> *)(tile + row0 * D + lds_at<D>(lane & 31, 2 * k + (lane >> 5)));
 }
 
 // Operand A of the transpose: rows = elements 32 d .. + 31 of the tile's rows,
-// contraction = tile rows row0 .. + 15 in the order of a score register run.
+// contraction = tile rows row0 .. + 15 (row0 a multiple of 16) in the order of a
+// score register run. The rows 8 further on have the swizzle of these ^ 2.
 template <class E, int D>
 __device__ __forceinline__ frag<E> lds_cols(const E *tile, int row0, int d, int lane) {
-  const int r = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-  const int e = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      LDS_PTR(i16x4, tile + lds_at<D>(r, e >> 3) + (e & 7)));
-  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      LDS_PTR(i16x4, tile + lds_at<D>(r + 8, e >> 3) + (e & 7)));
+  const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+  const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = 4 * (lane & 1);
+  const E *at = tile + row0 * D + in;
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, at + lds_at<D>(r, c)));
+  const i16x4 b =
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, at + 8 * D + lds_at<D>(r, c ^ 2)));
   return __builtin_bit_cast(frag<E>, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 

@@ -74,17 +74,21 @@ struct Softmax {
                                        const int2 (&span)[NQ], bool full, int key0,
                                        float scale_log2, int lane) {
     f32x16 s[NQ][NS];
+    frag<E> a[NS][D / 16];
 #pragma unroll
-    for (int b = 0; b < NS; b++) {
+    for (int k = 0; k < D / 16; k++)
 #pragma unroll
-      for (int n = 0; n < NQ; n++) s[n][b] = 0.0f;
+      for (int b = 0; b < NS; b++) a[b][k] = lds_rows<E, D>(kt, 32 * b, k, lane);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = 0; k < D / 16; k++) {
-        const frag<E> a = lds_rows<E, D>(kt, 32 * b, k, lane);
+    for (int k = 0; k < D / 16; k++)
 #pragma unroll
-        for (int n = 0; n < NQ; n++) s[n][b] = mfma(a, q[n][k], s[n][b]);
-      }
-    }
+      for (int n = 0; n < NQ; n++)
+#pragma unroll
+        for (int b = 0; b < NS; b++) {
+          if (k == 0) s[n][b] = 0.0f;
+          s[n][b] = mfma(a[b][k], q[n][k], s[n][b]);
+        }
     if (!full) {
 #pragma unroll
       for (int n = 0; n < NQ; n++)
@@ -97,6 +101,13 @@ struct Softmax {
               s[n][b][i] = -INFINITY;
           }
     }
+    // the first half's values, on their way while the softmax is computed
+    frag<E> v0[2][D / 32];
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+#pragma unroll
+      for (int d = 0; d < D / 32; d++) v0[k][d] = lds_cols<E, D>(vt, 16 * k, d, lane);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < NQ; n++) {
       float top = s[n][0][0];
@@ -124,36 +135,41 @@ struct Softmax {
         }
       l[n] += sum;
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int b = 0; b < NS; b++)
+    for (int b = 0; b < NS; b++) {
+      frag<E> c[2][D / 32];
 #pragma unroll
-      for (int k = 0; k < 2; k++) {
-        frag<E> w[NQ];
+      for (int k = 0; k < 2; k++)
 #pragma unroll
-        for (int n = 0; n < NQ; n++) w[n] = pack8<E>(s[n][b], k);
+        for (int d = 0; d < D / 32; d++) c[k][d] = b ? lds_cols<E, D>(vt, 32 * b + 16 * k, d, lane) : v0[k][d];
 #pragma unroll
-        for (int d = 0; d < D / 32; d++) {
-          const frag<E> a = lds_cols<E, D>(vt, 32 * b + 16 * k, d, lane);
+      for (int k = 0; k < 2; k++)
 #pragma unroll
-          for (int n = 0; n < NQ; n++) o[n][d] = mfma(a, w[n], o[n][d]);
+        for (int n = 0; n < NQ; n++) {
+          const frag<E> w = pack8<E>(s[n][b], k);
+#pragma unroll
+          for (int d = 0; d < D / 32; d++) o[n][d] = mfma(c[k][d], w, o[n][d]);
         }
-      }
+    }
   }
 };
 
 // ------------------------------------------------------------ many rows
 // A block of four waves takes 128 NQ queries of one head and streams the keys
-// and values of their spans through LDS in tiles of 64, two tiles in flight: the
-// next one in registers while this one is computed.
+// and values of their spans through LDS in tiles of 64, the next one on its way
+// while this one is computed.
 template <class E, int D, int NQ>
 __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p, int tiles) {
-  __shared__ __attribute__((aligned(16))) E lds[2][2][KT * D];
+  // Objects of their own, and turns of the loop that name theirs: the compiler then
+  // sees that reads of one do not wait for copies into the other.
+  using Buf = E[2][KT * D];
+  __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = die_order(blockIdx.x, gridDim.x);
-  const int bh = item / tiles, b = bh / p.q_heads, head = bh - b * p.q_heads;
-  // causal rows see more keys the later they are: the longest blocks first
-  const int tile = p.causal ? tiles - 1 - (item - bh * tiles) : item - bh * tiles;
+  const int2 bt = block_item(p, item, p.batch * p.q_heads, tiles);
+  const int bh = bt.x, tile = bt.y, b = bh / p.q_heads, head = bh - b * p.q_heads;
   const int kvh = head / p.share, row0 = tile * 128 * NQ + wave * 32 * NQ + (lane & 31);
 
   frag<E> q[NQ][D / 16];
@@ -198,29 +214,25 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
   Softmax<E, D, NQ> sm;
   sm.init();
-  Staged<E, D, 256, KT> sk, sv;
+  using Tile = Copy<E, D, 256, KT>;
   if (first < end) {
-    sk.load(ks, first * KT, tid);
-    sv.load(vs, first * KT, tid);
-    sk.store(lds[0][0], tid);
-    sv.store(lds[0][1], tid);
+    Tile::issue(ks, first * KT, b0[0], tid);
+    Tile::issue(vs, first * KT, b0[1], tid);
   }
-  __syncthreads();
-  for (int j = first; j < end; j++) {
-    const int at = (j - first) & 1;
+  auto turn = [&](int j, Buf &here, Buf &there) {
+    block_copied();  // tile j is there, and nobody reads the other one any more
     if (j + 1 < end) {
-      sk.load(ks, (j + 1) * KT, tid);
-      sv.load(vs, (j + 1) * KT, tid);
+      Tile::issue(ks, (j + 1) * KT, there[0], tid);
+      Tile::issue(vs, (j + 1) * KT, there[1], tid);
     }
     const int key0 = j * KT;
     if (key0 < hi && key0 + KT > lo)
-      sm.template tile<KT / 32>(lds[at][0], lds[at][1], q, span,
-                                key0 >= in_lo && key0 + KT <= in_hi, key0, p.scale_log2, lane);
-    if (j + 1 < end) {
-      sk.store(lds[at ^ 1][0], tid);
-      sv.store(lds[at ^ 1][1], tid);
-    }
-    __syncthreads();
+      sm.template tile<KT / 32>(here[0], here[1], q, span, key0 >= in_lo && key0 + KT <= in_hi,
+                                key0, p.scale_log2, lane);
+  };
+  for (int j = first; j < end; j += 2) {
+    turn(j, b0, b1);
+    if (j + 1 < end) turn(j + 1, b1, b0);
   }
 
 #pragma unroll
@@ -276,7 +288,8 @@ constexpr int FT = 32;
 template <class E, int D>
 __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   // per wave two tiles of keys and values; afterwards m, l and o of the waves
-  __shared__ __attribute__((aligned(16))) E lds[4][2][2][FT * D];
+  using Buf = E[4][2][FT * D];
+  __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ float ml[4][2][32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int item = die_order(blockIdx.x, gridDim.x);
@@ -307,28 +320,30 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
   Softmax<E, D, 1> sm;
   sm.init();
-  Staged<E, D, 64, FT> sk, sv;
+  using Tile = Copy<E, D, 64, FT>;
   const int first = __builtin_amdgcn_readfirstlane(lo < hi ? lo / FT + wave : 0);
   const int end = __builtin_amdgcn_readfirstlane(lo < hi ? (hi + FT - 1) / FT : 0);
   if (first < end) {
-    sk.load(ks, first * FT, lane);
-    sv.load(vs, first * FT, lane);
+    Tile::issue(ks, first * FT, b0[wave][0], lane);
+    Tile::issue(vs, first * FT, b0[wave][1], lane);
   }
-  int at = 0;
-  for (int j = first; j < end; j += 4, at ^= 1) {
-    sk.store(lds[wave][at][0], lane);
-    sv.store(lds[wave][at][1], lane);
+  auto turn = [&](int j, Buf &here, Buf &there) {
     if (j + 4 < end) {
-      sk.load(ks, (j + 4) * FT, lane);
-      sv.load(vs, (j + 4) * FT, lane);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the buffer's last reads are done
+      Tile::issue(ks, (j + 4) * FT, there[wave][0], lane);
+      Tile::issue(vs, (j + 4) * FT, there[wave][1], lane);
+      copied<2 * Tile::N>();
+    } else {
+      copied<0>();
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_order();
     const int key0 = j * FT;
     const bool full = key0 >= in_lo && key0 + FT <= in_hi && key0 >= p0 && key0 + FT <= p1;
-    sm.template tile<1>(lds[wave][at][0], lds[wave][at][1], q, span, full, key0, p.scale_log2,
-                        lane);
+    sm.template tile<1>(here[wave][0], here[wave][1], q, span, full, key0, p.scale_log2, lane);
+  };
+  for (int j = first; j < end; j += 8) {
+    turn(j, b0, b1);
+    if (j + 4 < end) turn(j + 4, b1, b0);
   }
 
   // Join the waves: a common reference, then sums in LDS in wave order.
@@ -346,7 +361,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   for (int w = 0; w < 4; w++)
     l += ml[w][1][lane & 31] * __builtin_amdgcn_exp2f(ml[w][0][lane & 31] - ref);
   const float mine = __builtin_amdgcn_exp2f(sm.m[0] - ref);
-  float *sum = (float *)&lds[0][0][0][0];  // [32][D + 4]
+  float *sum = (float *)&b0[0][0][0];  // [32][D + 4]
   for (int w = 0; w < 4; w++) {
     if (w == wave) {
       float *to = sum + (lane & 31) * (D + 4);
@@ -408,25 +423,41 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   }
 }
 
-// Joins the parts of one row: a wave a row, two elements a lane.
+// Joins the parts of one row: a block a row, 32 lanes with four elements each for
+// every eighth part.
 template <class E>
 __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t all = (int64_t)p.batch * p.q_heads * p.q_len;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= all) return;
+  __shared__ float tops[4];
+  __shared__ __attribute__((aligned(16))) float sums[8][132];
+  const int tid = threadIdx.x, lane = tid & 63, e = 4 * (tid & 31);
+  const int64_t all = (int64_t)p.batch * p.q_heads * p.q_len, row = blockIdx.x;
   float top = -INFINITY;
-  for (int s = lane; s < p.splits; s += 64) top = fmaxf(top, p.part_ml[2 * (s * all + row)]);
+  for (int s = tid; s < p.splits; s += 256) top = fmaxf(top, p.part_ml[2 * (s * all + row)]);
   top = wave_fmax(top);
+  if (lane == 0) tops[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
   const float ref = top == -INFINITY ? 0.0f : top;
-  float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+  float l = 0.0f;
+  f32x4 o = 0.0f;
 #pragma unroll 4
-  for (int s = 0; s < p.splits; s++) {
+  for (int s = tid >> 5; s < p.splits; s += 8) {
     const int64_t slot = s * all + row;
     const float w = __builtin_amdgcn_exp2f(p.part_ml[2 * slot] - ref);
     l = fmaf(p.part_ml[2 * slot + 1], w, l);
-    if (lane < p.dim) o0 = fmaf(p.part_o[slot * p.dim + lane], w, o0);
-    if (lane + 64 < p.dim) o1 = fmaf(p.part_o[slot * p.dim + lane + 64], w, o1);
+    if (e < p.dim) o += *(const f32x4 *)(p.part_o + slot * p.dim + e) * w;
+  }
+  *(f32x4 *)&sums[tid >> 5][e] = o;
+  if ((tid & 31) == 0) sums[tid >> 5][128] = l;
+  __syncthreads();
+  if (tid >= 64) return;
+  l = 0.0f;
+  float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    l += sums[i][128];
+    o0 += sums[i][lane];
+    o1 += sums[i][lane + 64];
   }
   const int64_t bh = row / p.q_len;
   const int t = (int)(row - bh * p.q_len), b = (int)(bh / p.q_heads);
@@ -436,9 +467,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  E *o = tok_row<E>(p.o, b, t, head);
-  if (lane < p.dim) o[lane] = (E)(o0 * inv);
-  if (lane + 64 < p.dim) o[lane + 64] = (E)(o1 * inv);
+  E *to = tok_row<E>(p.o, b, t, head);
+  if (lane < p.dim) to[lane] = (E)(o0 * inv);
+  if (lane + 64 < p.dim) to[lane + 64] = (E)(o1 * inv);
   if (lane == 0)
     p.lse[row] = l == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * ATTN_LN2;
 }
@@ -451,7 +482,7 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
-    k_attn_join<E><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(p);
+    k_attn_join<E><<<(unsigned)rows, 256, 0, st>>>(p);
     return hipGetLastError();
   }
   const int tiles = (p.q_len + 127) / 128;
@@ -469,7 +500,7 @@ void gs_attn_plan(AttnK *p) {
   const int64_t many = (int64_t)p->batch * p->q_heads * ((p->q_len + 127) / 128);
   p->splits = 0;
   p->split_keys = 0;
-  if (!p->batch || !p->q_len || (rows > 32 && many >= 128)) return;
+  if (!p->batch || !p->q_len || (rows > 32 && many >= 256)) return;
   const int64_t blocks = (int64_t)p->batch * p->kv_heads * row_tiles;
   // about 512 workgroups, none with fewer than 256 keys
   int64_t splits = (512 + blocks - 1) / blocks;

@@ -35,8 +35,8 @@ __device__ __forceinline__ Words philox(uint64_t ctr, uint64_t key) {
 }
 
 // Contiguous arrays on 16-byte boundaries: a thread takes 8 elements, two
-// generator blocks; per_row: 8 elements of one row (cols a multiple of 8), one
-// block.
+// generator blocks, and one thread the last count % 8; per_row: 8 elements of one
+// row (cols a multiple of 8), one block.
 template <class E, bool RES, bool ROW>
 __global__ __launch_bounds__(256) void k_dropout_vec(DropK p, int64_t n8) {
   const int64_t step = (int64_t)gridDim.x * 256;
@@ -69,6 +69,15 @@ __global__ __launch_bounds__(256) void k_dropout_vec(DropK p, int64_t n8) {
     }
     store4((E *)p.y + 8 * i, y0);
     store4((E *)p.y + 8 * i + 4, y1);
+  }
+  if (ROW || blockIdx.x || threadIdx.x) return;
+  const int64_t n = p.rows * p.cols;
+  for (int64_t i = 8 * n8; i < n; i++) {
+    const Words w = philox(p.offset + (uint64_t)(i >> 2), p.seed);
+    const uint32_t m = i & 2 ? (i & 1 ? w.w[3] : w.w[2]) : (i & 1 ? w.w[1] : w.w[0]);
+    float y = m >= p.drop_below ? (float)((const E *)p.x)[i] * p.scale : 0.0f;
+    if (RES) y += (float)((const E *)p.res)[i];
+    ((E *)p.y)[i] = (E)y;
   }
 }
 
@@ -116,7 +125,7 @@ void launch_type(const DropK &p, hipStream_t st) {
   const bool flat = p.rows == 1 || (p.x_stride == p.cols && p.y_stride == p.cols &&
                                     (!p.res || p.res_stride == p.cols));
   const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.res | (uintptr_t)p.y;
-  const bool vector = flat && at % 16 == 0 && (p.per_row ? p.cols : n) % 8 == 0;
+  const bool vector = flat && at % 16 == 0 && n >= 8 && (!p.per_row || p.cols % 8 == 0);
   if (p.res) launch<E, true>(p, vector, st);
   else launch<E, false>(p, vector, st);
 }

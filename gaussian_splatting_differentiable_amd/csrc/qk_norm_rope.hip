@@ -214,22 +214,31 @@ __global__ __launch_bounds__(256) void k_qk_bwd(QkK p) {
   }
 }
 
-// The weight gradients: 16 columns a block, their partial sums added by 16 lanes
+// The weight gradients: 16 columns a block, their partial sums added by 64 threads
 // each in a fixed order.
-__global__ __launch_bounds__(256) void k_qk_weights(QkK p) {
-  __shared__ float sums[16][17];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+__global__ __launch_bounds__(1024) void k_qk_weights(QkK p) {
+  __shared__ float sums[64][17];
+  const int c = threadIdx.x & 15, col = blockIdx.x * 16 + c, part = threadIdx.x >> 4;
   float *out = blockIdx.y ? p.dkw : p.dqw;
   if (!out) return;
   const float *in = p.partial + (int64_t)blockIdx.y * p.blocks * p.dim;
   float s = 0.0f;
   if (col < p.dim)
-    for (int i = part; i < p.blocks; i += 16) s += in[(int64_t)i * p.dim + col];
-  sums[part][threadIdx.x & 15] = s;
+#pragma unroll 4
+    for (int i = part; i < p.blocks; i += 64) s += in[(int64_t)i * p.dim + col];
+  sums[part][c] = s;
+  __syncthreads();
+  if (part < 8) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) s += sums[part * 8 + i][c];
+    sums[part * 8][c] = s;  // read by this thread alone until here
+  }
   __syncthreads();
   if (part == 0 && col < p.dim) {
     s = 0.0f;
-    for (int i = 0; i < 16; i++) s += sums[i][threadIdx.x & 15];
+#pragma unroll
+    for (int i = 0; i < 8; i++) s += sums[i * 8][c];
     out[col] = s;
   }
 }
@@ -250,7 +259,7 @@ int gs_qk_bwd_blocks(int64_t batch, int64_t tokens, int q_heads, int k_heads, in
   const int heads = q_heads > k_heads ? q_heads : k_heads;
   const int64_t groups = batch * tokens * ((heads + HC - 1) / HC);
   const int64_t blocks = (groups * lanes + 255) / 256;
-  return (int)(blocks < 1024 ? blocks : 1024);
+  return (int)(blocks < 512 ? blocks : 512);
 }
 
 hipError_t gs_launch_qk_fwd(const QkK &p, int dtype, hipStream_t st) {
@@ -269,6 +278,6 @@ hipError_t gs_launch_qk_bwd(const QkK &p, int dtype, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !(p.dqw || p.dkw)) return e;
-  k_qk_weights<<<dim3((p.dim + 15) / 16, 2), 256, 0, st>>>(p);
+  k_qk_weights<<<dim3((p.dim + 15) / 16, 2), 1024, 0, st>>>(p);
   return hipGetLastError();
 }

@@ -9,6 +9,7 @@ hipError_t gs_launch_qk_fwd(const QkK &p, int dtype, hipStream_t st);
 hipError_t gs_launch_qk_bwd(const QkK &p, int dtype, hipStream_t st);
 int gs_qk_bwd_blocks(int64_t batch, int64_t tokens, int q_heads, int k_heads, int lanes);
 void gs_attn_plan(AttnK *p);
+void gs_attn_bwd_plan(AttnK *p, bool masked);
 hipError_t gs_launch_attn_fwd(const AttnK &p, int dtype, hipStream_t st);
 hipError_t gs_launch_attn_bwd(const AttnK &p, int dtype, hipStream_t st);
 
@@ -155,6 +156,11 @@ size_t attn_bwd_layout(AttnK *p, bool masked, bool half, void *ws) {
   p->tile_spans = masked ? (int4 *)spans : nullptr;
   p->q_bound = (float *)part(half ? b * p->q_heads * qt * 8 : 0);
   p->v_bound = (float *)part(half ? b * p->kv_heads * kt * 4 : 0);
+  gs_attn_bwd_plan(p, masked);
+  const size_t q = b * p->q_heads * p->q_len * p->dim * 4, k = b * p->kv_heads * p->kv_len * p->dim * 4;
+  p->part_q = (float *)part(p->q_parts > 1 ? q * p->q_parts : 0);
+  p->part_k = (float *)part(p->kv_parts > 1 ? k * p->kv_parts : 0);
+  p->part_v = (float *)part(p->kv_parts > 1 ? k * p->kv_parts : 0);
   return total;
 }
 
@@ -228,7 +234,12 @@ size_t gs_attention_workspace_size(const gs_attn_shape *shape) {
 size_t gs_attention_bwd_workspace_size(const gs_attn_shape *shape) {
   AttnK p;
   if (attn_shape(shape, &p) != GS_OK) return 0;
-  return attn_bwd_layout(&p, true, shape->dtype == GS_F16, nullptr);
+  // with spans or without: the larger
+  AttnK n = p;
+  const bool half = shape->dtype == GS_F16;
+  const size_t a = attn_bwd_layout(&p, true, half, nullptr);
+  const size_t c = attn_bwd_layout(&n, false, half, nullptr);
+  return a > c ? a : c;
 }
 
 int32_t gs_attention(const gs_attn_shape *shape, const gs_tokens *q, const gs_tokens *k,

@@ -96,4 +96,6 @@ struct AttnK {
   float *delta;
   int4 *tile_spans;
   float *q_bound, *v_bound;
+  int q_parts, kv_parts;
+  float *part_q, *part_k, *part_v;
 };

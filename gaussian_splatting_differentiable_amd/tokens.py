@@ -13,39 +13,28 @@ calls for autograd.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 import math
+from struct import Struct
 
 import torch
 
-from . import GS_OK, GsError, _ptr, _stream, lib
+from . import GS_OK, GsError, lib
 
 F32, BF16, F16 = 0, 1, 2
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-class GsTokens(C.Structure):
-    _fields_ = [("data", C.c_void_p), ("batch_stride", C.c_int64), ("token_stride", C.c_int64),
-                ("head_stride", C.c_int64)]
-
-
-class GsQkShape(C.Structure):
-    _fields_ = [("batch", C.c_int32), ("tokens", C.c_int32), ("q_heads", C.c_int32),
-                ("k_heads", C.c_int32), ("dim", C.c_int32), ("dtype", C.c_int32),
-                ("rot_dim", C.c_int32), ("neighbours", C.c_int32), ("n_positions", C.c_int32),
-                ("eps", C.c_float), ("positions_stride", C.c_int64)]
-
-
-class GsAttnShape(C.Structure):
-    _fields_ = [("batch", C.c_int32), ("q_heads", C.c_int32), ("kv_heads", C.c_int32),
-                ("q_tokens", C.c_int32), ("kv_tokens", C.c_int32), ("dim", C.c_int32),
-                ("dtype", C.c_int32), ("causal", C.c_int32), ("scale", C.c_float),
-                ("spans_stride", C.c_int64)]
+# gs_tokens, gs_qk_shape and gs_attn_shape of include/gs.h as bytes, which ctypes passes
+# by address: building a Structure for every tensor costs more than a small call's kernel.
+_TOKENS, _QK, _ATTN = Struct("=4q"), Struct("=9ifq"), Struct("=8if4xq")
 
 
 def _declare(L):
     P, sz, i32, i64 = C.c_void_p, C.c_size_t, C.c_int32, C.c_int64
-    T, Q, A = C.POINTER(GsTokens), C.POINTER(GsQkShape), C.POINTER(GsAttnShape)
+    T = Q = A = C.c_char_p
     L.gs_qk_workspace_size.argtypes, L.gs_qk_workspace_size.restype = [Q], sz
     L.gs_attention_workspace_size.argtypes, L.gs_attention_workspace_size.restype = [A], sz
     L.gs_attention_bwd_workspace_size.argtypes = [A]
@@ -82,14 +71,19 @@ def _tokens(t):
     """The C view of a [batch, tokens, heads, dim] tensor (None: absent)."""
     if t is None:
         return None
-    return GsTokens(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    s = t.stride()
+    return _TOKENS.pack(t.data_ptr(), s[0], s[1], s[2])
 
 
 def _same(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.dim() == 4 and t.stride(3) != 1 and t.shape[3] != 1:
+    _inner(name, t)
+
+
+def _inner(name, t):
+    if t.stride(-1) != 1 and t.dim() == 4 and t.shape[3] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
 
 
@@ -100,19 +94,33 @@ def _base(name, t):
         raise ValueError(f"{name}: expected [batch, tokens, heads, dim]")
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name}: unsupported type {t.dtype}")
-    if t.stride(3) != 1 and t.shape[3] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    _inner(name, t)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream, *tensors):
     """The context calls allocate and launch in: the tensors' device and `stream`, on which
     the tensors are then marked as used."""
     if stream is None:
-        return torch.cuda.device(tensors[0].device)
+        device = tensors[0].device
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
     return torch.cuda.stream(stream)
+
+
+def _stream(stream, device):
+    """The handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _list2d(name, t, batch, n, tail, device):
@@ -123,18 +131,18 @@ def _list2d(name, t, batch, n, tail, device):
     if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 tensor on {device}")
     if t.shape == (n, *tail):
-        return C.c_void_p(t.data_ptr()), 0
+        return t.data_ptr(), 0
     if t.shape == (batch, n, *tail):
-        return C.c_void_p(t.data_ptr()), n
+        return t.data_ptr(), n
     raise ValueError(f"{name}: expected {(n, *tail)} or {(batch, n, *tail)}, got {tuple(t.shape)}")
 
 
 def _vector(name, t, n, device):
     if t is None:
         return None
-    if t.shape != (n,) or t.dtype != torch.float32 or t.device != device:
-        raise ValueError(f"{name}: expected {n} float32 values on {device}")
-    return _ptr(t)
+    if t.shape != (n,) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous float32 values on {device}")
+    return t.data_ptr()
 
 
 # ------------------------------------------------------------------ norm and rotation
@@ -149,12 +157,14 @@ def _qk_shape(q, k, cos_sin, positions, neighbours, eps):
         _same("k", k, (B, n, k.shape[2], d), q.dtype, q.device)
     rot = rows = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != x.device:
-            raise ValueError("cos_sin: expected [positions, rot_dim] float32 on the same device")
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != x.device \
+                or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin: expected contiguous [positions, rot_dim] float32 on the "
+                             "same device")
         rows, rot = cos_sin.shape
     pos, stride = _list2d("positions", positions, B, n, (), x.device)
-    shape = GsQkShape(B, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d,
-                      _DTYPES[x.dtype], rot, int(neighbours), rows, float(eps), stride)
+    shape = _QK.pack(B, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d,
+                     _DTYPES[x.dtype], rot, bool(neighbours), rows, eps, stride)
     return shape, x, pos
 
 
@@ -178,11 +188,10 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=
     shape, x, pos = _qk_shape(q, k, cos_sin, positions, neighbours, eps)
     wq = _vector("q_weight", q_weight, x.shape[3], x.device)
     wk = _vector("k_weight", k_weight, x.shape[3], x.device)
-    with _on(stream, *(t for t in (x, q, k, q_weight, k_weight, cos_sin, positions)
-                       if t is not None)):
+    with _on(stream, x, q, k, q_weight, k_weight, cos_sin, positions):
         q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-        _check(_lib().gs_qk_norm_rope(shape, _tokens(q), _tokens(k), wq, wk, _ptr(cos_sin), pos,
-                                      _tokens(q_out), _tokens(k_out), _stream(stream)),
+        _check(_lib().gs_qk_norm_rope(shape, _tokens(q), _tokens(k), wq, wk, _addr(cos_sin), pos,
+                                      _tokens(q_out), _tokens(k_out), _stream(stream, x.device)),
                "gs_qk_norm_rope")
     return q_out, k_out
 
@@ -198,8 +207,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_
             _same(name, g, t.shape, t.dtype, dev)
     wq, wk = _vector("q_weight", q_weight, d, dev), _vector("k_weight", k_weight, d, dev)
     L = _lib()
-    with _on(stream, *(t for t in (x, q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions)
-                       if t is not None)):
+    with _on(stream, x, q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions):
         dq, dk = _like(q), _like(k)
         dwq, dwk = (None if w is None else torch.empty(d, dtype=torch.float32, device=dev)
                     for w in (q_weight, k_weight))
@@ -209,9 +217,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_
             ws = torch.empty(size, dtype=torch.uint8, device=dev)
         _check(L.gs_qk_norm_rope_bwd(shape, _tokens(dq_out if q is not None else None),
                                      _tokens(dk_out if k is not None else None), _tokens(q),
-                                     _tokens(k), wq, wk, _ptr(cos_sin), pos, _tokens(dq),
-                                     _tokens(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), size,
-                                     _stream(stream)),
+                                     _tokens(k), wq, wk, _addr(cos_sin), pos, _tokens(dq),
+                                     _tokens(dk), _addr(dwq), _addr(dwk), _addr(ws), size,
+                                     _stream(stream, dev)),
                "gs_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -227,16 +235,20 @@ def _attn_shape(q, k, v, spans, causal, scale):
     at, stride = _list2d("spans", spans, B, n, (2,), q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return GsAttnShape(B, H, k.shape[2], n, k.shape[1], d, _DTYPES[q.dtype], int(causal),
-                       float(scale), stride), at
+    return _ATTN.pack(B, H, k.shape[2], n, k.shape[1], d, _DTYPES[q.dtype], bool(causal), scale,
+                      stride), at
 
 
 def attention_workspace_size(q, k, *, causal=False, backward=False) -> int:
     """Bytes of workspace an attention (or its backward) of these sizes takes."""
     shape, _ = _attn_shape(q, k, k, None, causal, None)
+    return _attn_bytes(shape, backward)
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_bytes(shape, backward):
     L = _lib()
-    return int((L.gs_attention_bwd_workspace_size if backward else
-                L.gs_attention_workspace_size)(shape))
+    return (L.gs_attention_bwd_workspace_size if backward else L.gs_attention_workspace_size)(shape)
 
 
 def _workspace(size, given, device):
@@ -257,14 +269,14 @@ def attention(q, k, v, *, spans=None, causal=False, scale=None, out=None, worksp
     query that sees no key gets 0 and lse = -inf. lse is [batch, q_heads, q_tokens] float32."""
     shape, at = _attn_shape(q, k, v, spans, causal, scale)
     L = _lib()
-    with _on(stream, *(t for t in (q, k, v, spans) if t is not None)):
+    with _on(stream, q, k, v, spans):
         o = _like(q, out)
         lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
                           device=q.device)
-        size = L.gs_attention_workspace_size(shape)
+        size = _attn_bytes(shape, False)
         ws = _workspace(size, workspace, q.device)
-        _check(L.gs_attention(shape, _tokens(q), _tokens(k), _tokens(v), at, _tokens(o), _ptr(lse),
-                              _ptr(ws), size, _stream(stream)),
+        _check(L.gs_attention(shape, _tokens(q), _tokens(k), _tokens(v), at, _tokens(o), _addr(lse),
+                              _addr(ws), size, _stream(stream, q.device)),
                "gs_attention")
     return o, lse
 
@@ -277,29 +289,28 @@ def attention_bwd(do, q, k, v, o, lse, *, spans=None, causal=False, scale=None, 
     _same("o", o, q.shape, q.dtype, q.device)
     _same("lse", lse, (q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device)
     L = _lib()
-    with _on(stream, *(t for t in (q, k, v, spans, do, o, lse) if t is not None)):
+    with _on(stream, q, k, v, spans, do, o, lse):
         dq, dk, dv = _like(q), _like(k), _like(k)
-        size = L.gs_attention_bwd_workspace_size(shape)
+        size = _attn_bytes(shape, True)
         ws = _workspace(size, workspace, q.device)
         _check(L.gs_attention_bwd(shape, _tokens(do), _tokens(q), _tokens(k), _tokens(v), at,
-                                  _tokens(o), _ptr(lse), _tokens(dq), _tokens(dk), _tokens(dv),
-                                  _ptr(ws), size, _stream(stream)),
+                                  _tokens(o), _addr(lse), _tokens(dq), _tokens(dk), _tokens(dv),
+                                  _addr(ws), size, _stream(stream, q.device)),
                "gs_attention_bwd")
     return dq, dk, dv
 
 
 # ------------------------------------------------------------------ dropout
 
-def _rows(t):
-    """(rows, cols, row stride) of a tensor seen as rows of its last dimension."""
-    if t.dim() < 2:
-        return (1, t.numel(), t.numel()) if t.dim() == 0 or t.is_contiguous() else \
-            (t.numel(), 1, t.stride(0))
+def _row_stride(name, t, rows, cols):
+    """Elements from one row to the next of t seen as [rows][cols]."""
     if t.is_contiguous():
-        return t.numel() // max(t.shape[-1], 1), t.shape[-1], t.shape[-1]
-    if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1):
-        return t.shape[0], t.shape[1], t.stride(0)
-    raise ValueError("expected a contiguous tensor, or two dimensions with contiguous rows")
+        return cols
+    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
+        return t.stride(0)
+    if t.dim() == 1:
+        return t.stride(0)
+    raise ValueError(f"{name}: expected a contiguous tensor, or rows that are contiguous")
 
 
 def dropout(x, p, seed, offset=0, *, residual=None, per_row=False, out=None, stream=None):
@@ -310,30 +321,27 @@ def dropout(x, p, seed, offset=0, *, residual=None, per_row=False, out=None, str
     ceil(draws / 4) counters from `offset` on."""
     if not x.is_cuda or x.dtype not in _DTYPES:
         raise ValueError("x: expected a float32, bfloat16 or float16 device tensor")
-    if per_row and x.dim() < 2:
+    if x.dim() > 1:
+        cols = x.shape[-1]
+        rows = x.numel() // cols if cols else 0
+    elif per_row:
         raise ValueError("per_row takes at least two dimensions")
-    rows, cols, xs = _rows(x)
-    with _on(stream, *(t for t in (x, residual) if t is not None)):
+    else:
+        rows, cols = x.numel(), 1
+    dev = x.device
+    with _on(stream, x, residual):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        strides = []
-        for name, t in (("residual", residual), ("out", out)):
-            if t is None:
-                strides.append(0)
-                continue
-            _same(name, t, x.shape, x.dtype, x.device)
-            r, c, s = _rows(t)
-            if (r, c) != (rows, cols):
-                r, c, s = (rows, cols, 1) if cols == 1 and t.is_contiguous() else (r, c, s)
-            if (r, c) != (rows, cols):
-                raise ValueError(f"{name}: its layout does not fit that of x")
-            strides.append(s)
-        _check(_lib().gs_dropout(rows, cols, _DTYPES[x.dtype], C.c_void_p(x.data_ptr()), xs,
-                                 None if residual is None else C.c_void_p(residual.data_ptr()),
-                                 strides[0], C.c_void_p(out.data_ptr()), strides[1], float(p),
-                                 seed & (2 ** 64 - 1), offset & (2 ** 64 - 1), int(per_row),
-                                 _stream(stream)),
-               "gs_dropout")
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _same("out", out, x.shape, x.dtype, dev)
+        if residual is not None:
+            _same("residual", residual, x.shape, x.dtype, dev)
+        _check(_lib().gs_dropout(
+            rows, cols, _DTYPES[x.dtype], x.data_ptr(), _row_stride("x", x, rows, cols),
+            _addr(residual),
+            0 if residual is None else _row_stride("residual", residual, rows, cols),
+            out.data_ptr(), _row_stride("out", out, rows, cols), p, seed & (2 ** 64 - 1),
+            offset & (2 ** 64 - 1), bool(per_row), _stream(stream, dev)), "gs_dropout")
     return out
 
 

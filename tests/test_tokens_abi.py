@@ -22,21 +22,21 @@ BAD, WORKSPACE, UNSUPPORTED = -1, -3, -5
 
 
 def _t(tok, at=1 << 20, b=1 << 16, t=512, h=64):
-    return tok.GsTokens(at, b, t, h)
+    return tok._TOKENS.pack(at, b, t, h)
 
 
 def _attn(tok, **kw):
     s = dict(batch=2, q_heads=4, kv_heads=2, q_tokens=64, kv_tokens=64, dim=64, dtype=tok.BF16,
              causal=0, scale=0.125, spans_stride=0)
     s.update(kw)
-    return tok.GsAttnShape(*(s[n] for n, _ in tok.GsAttnShape._fields_))
+    return tok._ATTN.pack(*s.values())
 
 
 def _qk(tok, **kw):
     s = dict(batch=2, tokens=16, q_heads=4, k_heads=2, dim=64, dtype=tok.BF16, rot_dim=32,
              neighbours=0, n_positions=16, eps=1e-6, positions_stride=0)
     s.update(kw)
-    return tok.GsQkShape(*(s[n] for n, _ in tok.GsQkShape._fields_))
+    return tok._QK.pack(*s.values())
 
 
 @pytest.mark.parametrize("kw,status", [
