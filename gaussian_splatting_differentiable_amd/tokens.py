@@ -68,10 +68,10 @@ def _check(status, what):
 
 
 def _tokens(t):
-    """The C view of a [batch, tokens, heads, dim] tensor (None: absent)."""
-    if t is None:
-        return None
+    """The C view of a [batch, tokens, heads, dim] tensor."""
     s = t.stride()
+    if s[3] != 1 and t.shape[3] != 1:
+        raise ValueError("the elements of a head must be contiguous")
     return _TOKENS.pack(t.data_ptr(), s[0], s[1], s[2])
 
 
@@ -79,43 +79,45 @@ def _same(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    _inner(name, t)
 
 
-def _inner(name, t):
-    if t.stride(-1) != 1 and t.dim() == 4 and t.shape[3] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
+def _whole(name, t, shape, dtype, device):
+    _same(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _base(name, t):
-    if not t.is_cuda:
+def _base(name, shape, dtype, device):
+    if device.type != "cuda":
         raise ValueError(f"{name}: expected a device tensor")
-    if t.dim() != 4:
+    if len(shape) != 4:
         raise ValueError(f"{name}: expected [batch, tokens, heads, dim]")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name}: unsupported type {t.dtype}")
-    _inner(name, t)
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name}: unsupported type {dtype}")
 
 
-_HERE = contextlib.nullcontext()
+def _elsewhere(stream, device):
+    """Whether a call is not for the current stream of the current device."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
-def _on(stream, *tensors):
-    """The context calls allocate and launch in: the tensors' device and `stream`, on which
-    the tensors are then marked as used."""
-    if stream is None:
-        device = tensors[0].device
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-    return torch.cuda.stream(stream)
+@contextlib.contextmanager
+def _there(stream, device, tensors):
+    """That stream and device, to allocate and launch in; the tensors are marked as used on it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            yield
 
 
-def _stream(stream, device):
-    """The handle of `stream`, or of the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
+def _stream(device):
+    """The handle of the device's current stream."""
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -126,8 +128,6 @@ def _addr(t):
 def _list2d(name, t, batch, n, tail, device):
     """(pointer, entries from one batch entry to the next) of an int32 list that is one per
     batch entry or shared by all."""
-    if t is None:
-        return None, 0
     if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 tensor on {device}")
     if t.shape == (n, *tail):
@@ -137,44 +137,64 @@ def _list2d(name, t, batch, n, tail, device):
     raise ValueError(f"{name}: expected {(n, *tail)} or {(batch, n, *tail)}, got {tuple(t.shape)}")
 
 
-def _vector(name, t, n, device):
-    if t is None:
-        return None
-    if t.shape != (n,) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous float32 values on {device}")
-    return t.data_ptr()
+def _out(name, out, like):
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _same(name, out, like.shape, like.dtype, like.device)
+    return out
 
 
 # ------------------------------------------------------------------ norm and rotation
 
-def _qk_shape(q, k, cos_sin, positions, neighbours, eps):
-    x = q if q is not None else k
-    if x is None:
+def _about(t):
+    return None if t is None else (t.shape, t.dtype, t.device)
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_plan(q, k, q_weight, k_weight, cos_sin, positions, neighbours, eps):
+    """The C shape from the (shape, type, device) of the tensors, and the workspace."""
+    if q is None and k is None:
         raise ValueError("queries or keys are needed")
-    _base("q" if q is not None else "k", x)
-    B, n, _, d = x.shape
+    (B, n, _, d), dt, dev = _sized("q", q) if q is not None else _sized("k", k)
     if q is not None and k is not None:
-        _same("k", k, (B, n, k.shape[2], d), q.dtype, q.device)
-    rot = rows = 0
+        (kb, kn, _, kd), kt, kdev = _sized("k", k)
+        if (kb, kn, kd, kt, kdev) != (B, n, d, dt, dev):
+            raise ValueError(f"q {q} and k {k} do not fit")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w != (torch.Size((d,)), torch.float32, dev):
+            raise ValueError(f"{name}: expected {d} float32 values on {dev}")
+    rot = rows = stride = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != x.device \
-                or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin: expected contiguous [positions, rot_dim] float32 on the "
-                             "same device")
-        rows, rot = cos_sin.shape
-    pos, stride = _list2d("positions", positions, B, n, (), x.device)
-    shape = _QK.pack(B, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], d,
-                     _DTYPES[x.dtype], rot, bool(neighbours), rows, eps, stride)
-    return shape, x, pos
+        if len(cos_sin[0]) != 2 or cos_sin[1:] != (torch.float32, dev):
+            raise ValueError(f"cos_sin: expected [positions, rot_dim] float32 on {dev}")
+        rows, rot = cos_sin[0]
+    if positions is not None:
+        if positions[0] not in ((n,), (B, n)) or positions[1:] != (torch.int32, dev):
+            raise ValueError(f"positions: expected {(n,)} or {(B, n)} int32 on {dev}")
+        stride = n if len(positions[0]) == 2 else 0
+    shape = _QK.pack(B, n, 0 if q is None else q[0][2], 0 if k is None else k[0][2], d,
+                     _DTYPES[dt], rot, neighbours, rows, eps, stride)
+    return shape, _lib().gs_qk_workspace_size(shape)
 
 
-def _like(t, out=None, name="out"):
-    if t is None:
-        return None
-    if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    _same(name, out, t.shape, t.dtype, t.device)
-    return out
+def _sized(name, about):
+    _base(name, *about)
+    return about
+
+
+def _qk_args(q, k, q_weight, k_weight, cos_sin, positions, neighbours, eps):
+    """(shape, workspace bytes, q view, k view, weight, table and position pointers, device)
+    after the checks."""
+    shape, size = _qk_plan(_about(q), _about(k), _about(q_weight), _about(k_weight),
+                           _about(cos_sin), _about(positions), bool(neighbours), eps)
+    at = []
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight), ("cos_sin", cos_sin),
+                    ("positions", positions)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        at.append(None if t is None else t.data_ptr())
+    return (shape, size, None if q is None else _tokens(q), None if k is None else _tokens(k), at,
+            (q if q is not None else k).device)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=None,
@@ -185,14 +205,18 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=
     cos_sin [positions, rot_dim] float32: cosines, then sines (None: no rotation); positions
     [batch, tokens] or [tokens] int32 rows of it (None: row t for token t). q_out, k_out may be
     the inputs. Returns (q_out, k_out)."""
-    shape, x, pos = _qk_shape(q, k, cos_sin, positions, neighbours, eps)
-    wq = _vector("q_weight", q_weight, x.shape[3], x.device)
-    wk = _vector("k_weight", k_weight, x.shape[3], x.device)
-    with _on(stream, x, q, k, q_weight, k_weight, cos_sin, positions):
-        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-        _check(_lib().gs_qk_norm_rope(shape, _tokens(q), _tokens(k), wq, wk, _addr(cos_sin), pos,
-                                      _tokens(q_out), _tokens(k_out), _stream(stream, x.device)),
-               "gs_qk_norm_rope")
+    shape, size, tq, tk, at, dev = _qk_args(q, k, q_weight, k_weight, cos_sin, positions,
+                                            neighbours, eps)
+    if _elsewhere(stream, dev):
+        with _there(stream, dev, (q, k, q_weight, k_weight, cos_sin, positions)):
+            return qk_norm_rope(q, k, q_weight, k_weight, cos_sin=cos_sin, positions=positions,
+                                neighbours=neighbours, eps=eps, q_out=q_out, k_out=k_out)
+    q_out = None if q is None else _out("q_out", q_out, q)
+    k_out = None if k is None else _out("k_out", k_out, k)
+    _check(_lib().gs_qk_norm_rope(shape, tq, tk, *at,
+                                  None if q is None else _tokens(q_out),
+                                  None if k is None else _tokens(k_out), _stream(dev)),
+           "gs_qk_norm_rope")
     return q_out, k_out
 
 
@@ -200,62 +224,75 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_
                      positions=None, neighbours=False, eps=1e-6, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) from those of qk_norm_rope's outputs; None for
     what was None."""
-    shape, x, pos = _qk_shape(q, k, cos_sin, positions, neighbours, eps)
-    d, dev = x.shape[3], x.device
-    for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if t is not None:
-            _same(name, g, t.shape, t.dtype, dev)
-    wq, wk = _vector("q_weight", q_weight, d, dev), _vector("k_weight", k_weight, d, dev)
+    shape, size, tq, tk, at, dev = _qk_args(q, k, q_weight, k_weight, cos_sin, positions,
+                                            neighbours, eps)
+    if _elsewhere(stream, dev):
+        with _there(stream, dev, (dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions)):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=cos_sin,
+                                    positions=positions, neighbours=neighbours, eps=eps)
+    dq = dk = gq = gk = oq = ok = dwq = dwk = ws = None
+    if q is not None:
+        _same("dq_out", dq_out, q.shape, q.dtype, dev)
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        gq, oq = _tokens(dq_out), _tokens(dq)
+    if k is not None:
+        _same("dk_out", dk_out, k.shape, k.dtype, dev)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        gk, ok = _tokens(dk_out), _tokens(dk)
+    if q_weight is not None:
+        dwq = torch.empty(q_weight.shape, dtype=torch.float32, device=dev)
+    if k_weight is not None:
+        dwk = torch.empty(k_weight.shape, dtype=torch.float32, device=dev)
     L = _lib()
-    with _on(stream, x, q, k, dq_out, dk_out, q_weight, k_weight, cos_sin, positions):
-        dq, dk = _like(q), _like(k)
-        dwq, dwk = (None if w is None else torch.empty(d, dtype=torch.float32, device=dev)
-                    for w in (q_weight, k_weight))
-        ws, size = None, 0
-        if dwq is not None or dwk is not None:
-            size = L.gs_qk_workspace_size(shape)
-            ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _check(L.gs_qk_norm_rope_bwd(shape, _tokens(dq_out if q is not None else None),
-                                     _tokens(dk_out if k is not None else None), _tokens(q),
-                                     _tokens(k), wq, wk, _addr(cos_sin), pos, _tokens(dq),
-                                     _tokens(dk), _addr(dwq), _addr(dwk), _addr(ws), size,
-                                     _stream(stream, dev)),
-               "gs_qk_norm_rope_bwd")
+    if dwq is not None or dwk is not None:
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _check(L.gs_qk_norm_rope_bwd(shape, gq, gk, tq, tk, *at, oq, ok, _addr(dwq), _addr(dwk),
+                                 _addr(ws), size, _stream(dev)),
+           "gs_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
 # ------------------------------------------------------------------ attention
 
-def _attn_shape(q, k, v, spans, causal, scale):
-    _base("q", q)
-    _base("k", k)
-    B, n, H, d = q.shape
-    _same("k", k, (B, k.shape[1], k.shape[2], d), q.dtype, q.device)
-    _same("v", v, k.shape, q.dtype, q.device)
-    at, stride = _list2d("spans", spans, B, n, (2,), q.device)
+@functools.lru_cache(maxsize=256)
+def _attn_plan(qs, ks, vs, types, devices, causal, scale, stride):
+    """What follows from the sizes: the C shape, that of the log sums, and the workspaces."""
+    _base("q", qs, types[0], devices[0])
+    _base("k", ks, types[1], devices[1])
+    B, n, H, d = qs
+    if ks[0] != B or ks[3] != d or vs != ks or len(set(types)) > 1 or len(set(devices)) > 1:
+        raise ValueError(f"q {tuple(qs)} {types[0]} on {devices[0]}, k {tuple(ks)} {types[1]} on "
+                         f"{devices[1]}, v {tuple(vs)} {types[2]} on {devices[2]} do not fit")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return _ATTN.pack(B, H, k.shape[2], n, k.shape[1], d, _DTYPES[q.dtype], bool(causal), scale,
-                      stride), at
+    shape = _ATTN.pack(B, H, ks[2], n, ks[1], d, _DTYPES[types[0]], causal, scale, stride)
+    L = _lib()
+    return (shape, (B, H, n), L.gs_attention_workspace_size(shape),
+            L.gs_attention_bwd_workspace_size(shape))
+
+
+def _attn_args(q, k, v, spans, causal, scale):
+    at, stride = None, 0
+    if spans is not None:
+        if q.dim() != 4:
+            raise ValueError("q: expected [batch, tokens, heads, dim]")
+        at, stride = _list2d("spans", spans, q.shape[0], q.shape[1], (2,), q.device)
+    return at, _attn_plan(q.shape, k.shape, v.shape, (q.dtype, k.dtype, v.dtype),
+                          (q.device, k.device, v.device), bool(causal), scale, stride)
 
 
 def attention_workspace_size(q, k, *, causal=False, backward=False) -> int:
     """Bytes of workspace an attention (or its backward) of these sizes takes."""
-    shape, _ = _attn_shape(q, k, k, None, causal, None)
-    return _attn_bytes(shape, backward)
-
-
-@functools.lru_cache(maxsize=256)
-def _attn_bytes(shape, backward):
-    L = _lib()
-    return (L.gs_attention_bwd_workspace_size if backward else L.gs_attention_workspace_size)(shape)
+    _, plan = _attn_args(q, k, k, None, causal, None)
+    return plan[3 if backward else 2]
 
 
 def _workspace(size, given, device):
     if given is None:
         return torch.empty(size, dtype=torch.uint8, device=device) if size else None
-    if given.numel() * given.element_size() < size:
-        raise ValueError(f"workspace: {size} bytes are needed")
+    if given.device != device or not given.is_contiguous() or \
+            given.numel() * given.element_size() < size:
+        raise ValueError(f"workspace: {size} contiguous bytes on {device} are needed")
     return given
 
 
@@ -267,48 +304,51 @@ def attention(q, k, v, *, spans=None, causal=False, scale=None, out=None, worksp
     float16; scale 1 / sqrt(dim) by default; spans [q_tokens, 2] or [batch, q_tokens, 2] int32:
     each query's keys [lo, hi); causal: query t sees keys up to t + kv_tokens - q_tokens. A
     query that sees no key gets 0 and lse = -inf. lse is [batch, q_heads, q_tokens] float32."""
-    shape, at = _attn_shape(q, k, v, spans, causal, scale)
-    L = _lib()
-    with _on(stream, q, k, v, spans):
-        o = _like(q, out)
-        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
-                          device=q.device)
-        size = _attn_bytes(shape, False)
-        ws = _workspace(size, workspace, q.device)
-        _check(L.gs_attention(shape, _tokens(q), _tokens(k), _tokens(v), at, _tokens(o), _addr(lse),
-                              _addr(ws), size, _stream(stream, q.device)),
-               "gs_attention")
+    at, (shape, rows, size, _) = _attn_args(q, k, v, spans, causal, scale)
+    dev = q.device
+    if _elsewhere(stream, dev):
+        with _there(stream, dev, (q, k, v, spans, out, workspace)):
+            return attention(q, k, v, spans=spans, causal=causal, scale=scale, out=out,
+                             workspace=workspace)
+    o = _out("out", out, q)
+    lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    ws = _workspace(size, workspace, dev) if size else None
+    _check(_lib().gs_attention(shape, _tokens(q), _tokens(k), _tokens(v), at, _tokens(o),
+                               lse.data_ptr(), _addr(ws), size, _stream(dev)),
+           "gs_attention")
     return o, lse
 
 
 def attention_bwd(do, q, k, v, o, lse, *, spans=None, causal=False, scale=None, workspace=None,
                   stream=None):
     """Gradients (dq, dk, dv) of attention from that of o, with its o and lse."""
-    shape, at = _attn_shape(q, k, v, spans, causal, scale)
-    _same("do", do, q.shape, q.dtype, q.device)
-    _same("o", o, q.shape, q.dtype, q.device)
-    _same("lse", lse, (q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device)
-    L = _lib()
-    with _on(stream, q, k, v, spans, do, o, lse):
-        dq, dk, dv = _like(q), _like(k), _like(k)
-        size = _attn_bytes(shape, True)
-        ws = _workspace(size, workspace, q.device)
-        _check(L.gs_attention_bwd(shape, _tokens(do), _tokens(q), _tokens(k), _tokens(v), at,
-                                  _tokens(o), _addr(lse), _tokens(dq), _tokens(dk), _tokens(dv),
-                                  _addr(ws), size, _stream(stream, q.device)),
-               "gs_attention_bwd")
+    at, (shape, rows, _, size) = _attn_args(q, k, v, spans, causal, scale)
+    dev = q.device
+    _same("do", do, q.shape, q.dtype, dev)
+    _same("o", o, q.shape, q.dtype, dev)
+    sums = _whole("lse", lse, rows, torch.float32, dev)
+    if _elsewhere(stream, dev):
+        with _there(stream, dev, (do, q, k, v, o, lse, spans, workspace)):
+            return attention_bwd(do, q, k, v, o, lse, spans=spans, causal=causal, scale=scale,
+                                 workspace=workspace)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    ws = _workspace(size, workspace, dev)
+    _check(_lib().gs_attention_bwd(shape, _tokens(do), _tokens(q), _tokens(k), _tokens(v), at,
+                                   _tokens(o), sums, _tokens(dq), _tokens(dk), _tokens(dv),
+                                   _addr(ws), size, _stream(dev)),
+           "gs_attention_bwd")
     return dq, dk, dv
 
 
 # ------------------------------------------------------------------ dropout
 
-def _row_stride(name, t, rows, cols):
-    """Elements from one row to the next of t seen as [rows][cols]."""
+def _row_stride(name, t, cols):
+    """Elements from one row to the next of t seen as rows of `cols`."""
     if t.is_contiguous():
         return cols
-    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
-        return t.stride(0)
-    if t.dim() == 1:
+    if t.dim() == 1 or (t.dim() == 2 and (t.stride(1) == 1 or cols == 1)):
         return t.stride(0)
     raise ValueError(f"{name}: expected a contiguous tensor, or rows that are contiguous")
 
@@ -319,8 +359,12 @@ def dropout(x, p, seed, offset=0, *, residual=None, per_row=False, out=None, str
     per_row: one draw for each row (the last dimension) instead of each element. The gradient
     with respect to x is dropout(dy, p, seed, offset, per_row=...). A call takes
     ceil(draws / 4) counters from `offset` on."""
-    if not x.is_cuda or x.dtype not in _DTYPES:
+    dev = x.device
+    if dev.type != "cuda" or x.dtype not in _DTYPES:
         raise ValueError("x: expected a float32, bfloat16 or float16 device tensor")
+    if _elsewhere(stream, dev):
+        with _there(stream, dev, (x, residual, out)):
+            return dropout(x, p, seed, offset, residual=residual, per_row=per_row, out=out)
     if x.dim() > 1:
         cols = x.shape[-1]
         rows = x.numel() // cols if cols else 0
@@ -328,20 +372,14 @@ def dropout(x, p, seed, offset=0, *, residual=None, per_row=False, out=None, str
         raise ValueError("per_row takes at least two dimensions")
     else:
         rows, cols = x.numel(), 1
-    dev = x.device
-    with _on(stream, x, residual):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            _same("out", out, x.shape, x.dtype, dev)
-        if residual is not None:
-            _same("residual", residual, x.shape, x.dtype, dev)
-        _check(_lib().gs_dropout(
-            rows, cols, _DTYPES[x.dtype], x.data_ptr(), _row_stride("x", x, rows, cols),
-            _addr(residual),
-            0 if residual is None else _row_stride("residual", residual, rows, cols),
-            out.data_ptr(), _row_stride("out", out, rows, cols), p, seed & (2 ** 64 - 1),
-            offset & (2 ** 64 - 1), bool(per_row), _stream(stream, dev)), "gs_dropout")
+    out = _out("out", out, x)
+    if residual is not None:
+        _same("residual", residual, x.shape, x.dtype, dev)
+    _check(_lib().gs_dropout(
+        rows, cols, _DTYPES[x.dtype], x.data_ptr(), _row_stride("x", x, cols), _addr(residual),
+        0 if residual is None else _row_stride("residual", residual, cols), out.data_ptr(),
+        _row_stride("out", out, cols), p, seed & (2 ** 64 - 1), offset & (2 ** 64 - 1),
+        bool(per_row), _stream(dev)), "gs_dropout")
     return out
 
 
