@@ -41,7 +41,8 @@ __device__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
   const int kvh = head / p.share;
   const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
   const E *q = tok_row<E>(p.q, b, t, head), *g = tok_row<E>(p.d_o, b, t, head);
-  const float lse = p.lse[at] * ATTN_LOG2E, delta = p.delta[at];
+  const float lse = p.lse[at] * ATTN_LOG2E;
+  const float delta = -p.row_delta[((int64_t)b * p.q_heads + head) * p.q_pad + t];
   float a0 = 0.0f, a1 = 0.0f;
   for (int j0 = span.x; j0 < span.y; j0 += 64) {
     const int n = min(64, span.y - j0);
@@ -79,7 +80,8 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int lane) {
         const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
         const float s = dot_row(tok_row<E>(p.q, b, t, head), k, p.dim) * p.scale_log2;
         w = __builtin_amdgcn_exp2f(s - p.lse[at] * ATTN_LOG2E);
-        ds = w * (dot_row(tok_row<E>(p.d_o, b, t, head), v, p.dim) - p.delta[at]);
+        ds = w * (dot_row(tok_row<E>(p.d_o, b, t, head), v, p.dim) +
+                  p.row_delta[((int64_t)b * p.q_heads + head) * p.q_pad + t]);
       }
       while (todo) {
         const int j = __builtin_ctzll(todo);
@@ -108,8 +110,10 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int lane) {
 }
 
 // ------------------------------------------------------------ preparation
-// D_i; for each 64 queries the keys that some row sees and that all see (lo, hi,
-// in_lo, in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
+// The rows' values as dK and dV start from them, in whole tiles (rows past the end
+// and rows that see nothing: -inf, which gives p = 0); with masks the rows' spans, and
+// for each 64 queries the keys that some row sees and that all see (lo, hi, in_lo,
+// in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
 // largest |v_j| of each 64 keys. 16 lanes a row.
 template <class E>
 __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_tiles) {
@@ -127,6 +131,7 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
       const int4 r = {wave_min(some ? s.x : INT32_MAX), wave_max(s.y), wave_max(on ? s.x : 0),
                       wave_min(on ? s.y : INT32_MAX)};
       if (lane == 0) p.tile_spans[(int64_t)b * q_tiles + qt] = r;
+      p.row_spans[(int64_t)b * p.q_pad + t] = s;
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -143,7 +148,14 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
         }
       }
       d = group_sum(d, 16);
-      if (t < p.q_len && j == 0) p.delta[((int64_t)b * p.q_heads + head) * p.q_len + t] = d;
+      if (j == 0) {
+        const int64_t at = (int64_t)bh * p.q_pad + t;
+        const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
+        p.row_delta[at] = -d;
+        p.row_lse[at] = lse == -INFINITY
+                            ? -INFINITY
+                            : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
+      }
       if (is_half<E>) {
         m0 = fmaxf(m0, sqrtf(group_sum(n, 16)));
         m1 = fmaxf(m1, fabsf(d));
@@ -187,15 +199,19 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
   }
 }
 
-// Largest of n floats at x, `stride` apart, by a block of 256 threads.
+// Largest of n floats at x, `stride` apart, by a block of NT threads.
+template <int NT>
 __device__ __forceinline__ float block_top(const float *x, int64_t n, int stride, float *lds) {
   float m = 0.0f;
-  for (int64_t i = threadIdx.x; i < n; i += 256) m = fmaxf(m, x[i * stride]);
+  for (int64_t i = threadIdx.x; i < n; i += NT) m = fmaxf(m, x[i * stride]);
   m = wave_fmax(m);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
   __syncthreads();
-  return fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+  m = lds[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; w++) m = fmaxf(m, lds[w]);
+  return m;
 }
 
 // Stores a transposed accumulator (lane: a row, registers: its elements) and
@@ -238,58 +254,57 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[D / 32], float by
 }
 
 // ------------------------------------------------------------ dK and dV
-// A block owns 128 keys of one key head, a wave 32 of them (K and V as operands in
-// registers), and streams the queries that see them in tiles of 64, head after
-// head of those that share the key head. Where there are too few such blocks, or
-// masks make them uneven, a block takes one of kv_parts equal runs of those tiles,
-// and k_attn_sum adds the parts' 32-bit sums.
-//
-// The steps of one 32 x 32 block are spread over two turns of the loop, so that
-// the vector unit and the matrix unit work at the same time in the one wave that
-// a SIMD has room for (D = 128: K, V, dK, dV and two sets of operands take most
-// of the 512 registers): a turn computes the scores of block s, then its
-// probabilities while the matrix unit adds block s - 1 to dK and dV and the rows
-// of block s + 1 arrive from LDS. -lse / scale and -D_i are the accumulators'
-// starting values.
+// A block of eight waves owns 128 keys of one key head and streams the queries that
+// see them in tiles of 64, head after head of those that share the key head: wave w
+// takes keys 32 (w % 4) .. + 31 and rows 32 (w / 4) .. + 31 of every tile, so that
+// each SIMD has two waves whose matrix and vector work overlap. K and V stay in LDS
+// (beside dK and dV a wave's 256 registers have no room for them). Where there are too few such blocks, or masks make them uneven, a block takes
+// one of kv_parts equal runs of those tiles, and k_attn_sum adds the parts' 32-bit
+// sums. -lse / scale and -D_i are the accumulators' starting values.
 template <class E, int D>
-__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, int tiles,
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
                                                                        int q_tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
   // sees that reads of one do not wait for copies into another.
   using Buf = E[2][KT * D];
-  __shared__ __attribute__((aligned(16))) Buf b0, b1, b2;
-  __shared__ __attribute__((aligned(16))) float stat[3][2][KT];
-  __shared__ __attribute__((aligned(16))) int2 spans[3][KT];
-  __shared__ uint64_t active[WALK / 64], partial[WALK / 64];
-  __shared__ float tops[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) Buf b0, b1;
+  __shared__ __attribute__((aligned(16))) E own_k[128 * D], own_v[128 * D];
+  __shared__ __attribute__((aligned(16))) float stat[2][2][KT];
+  __shared__ __attribute__((aligned(16))) int2 spans[2][KT];
+  __shared__ uint64_t active[WALK / 64];
+  __shared__ uint16_t list[WALK];
+  __shared__ float tops[8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = wave >> 2;
   const int item = die_order(blockIdx.x, gridDim.x);
   const int piece = item % p.kv_parts, whole = item / p.kv_parts;
   const int bh = whole / tiles, b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
-  const int key0 = (whole - bh * tiles) * 128, mine0 = key0 + 32 * wave;
+  const int key0 = (whole - bh * tiles) * 128, mine0 = key0 + 32 * (wave & 3);
   const int key = mine0 + (lane & 31);
   const bool on = key < p.kv_len;
 
-  frag<E> kf[D / 16], vf[D / 16];
   {
-    const E *kr = tok_row<E>(p.k, b, on ? key : 0, kvh), *vr = tok_row<E>(p.v, b, on ? key : 0, kvh);
+    const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
+    const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
 #pragma unroll
-    for (int k = 0; k < D / 16; k++) {
-      const int chunk = 2 * k + (lane >> 5);
-      kf[k] = row_operand<E>(kr, chunk, on && 8 * chunk < p.dim);
-      vf[k] = row_operand<E>(vr, chunk, on && 8 * chunk < p.dim);
+    for (int i = 0; i < 128; i += 64) {
+      Copy<E, D, 512, 64>::issue(ks, key0 + i, own_k + i * D, tid);
+      Copy<E, D, 512, 64>::issue(vs, key0 + i, own_v + i * D, tid);
     }
   }
   int e = 0;
   if (is_half<E>) {
     const float *qb = p.q_bound + 2 * ((int64_t)b * p.q_heads + kvh * p.share) * q_tiles;
-    const float g = block_top(qb, (int64_t)p.share * q_tiles, 2, tops);
-    const float d = block_top(qb + 1, (int64_t)p.share * q_tiles, 2, tops);
+    const float g = block_top<512>(qb, (int64_t)p.share * q_tiles, 2, tops);
+    const float d = block_top<512>(qb + 1, (int64_t)p.share * q_tiles, 2, tops);
+    block_copied();
     float n = 0.0f;
 #pragma unroll
-    for (int k = 0; k < D / 16; k++)
+    for (int k = 0; k < D / 16; k++) {
+      const frag<E> v = lds_rows<E, D>(own_v, 32 * (wave & 3), k, lane);
 #pragma unroll
-      for (int i = 0; i < 8; i++) n = fmaf((float)vf[k][i], (float)vf[k][i], n);
+      for (int i = 0; i < 8; i++) n = fmaf((float)v[i], (float)v[i], n);
+    }
     e = headroom(g * sqrtf(other_half(n, false)) + d);
   }
   const float ds_by = is_half<E> ? ldexpf(1.0f, e - 15) : 1.0f;
@@ -299,210 +314,196 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_attn_bwd_kv(AttnK p, i
   for (int d = 0; d < D / 32; d++) dk[d] = dv[d] = 0.0f;
 
   for (int walk0 = 0; walk0 < q_tiles; walk0 += WALK) {
-    // Which of the next WALK tiles see a key of this block, and which of them not
-    // all of its keys with all of their rows.
-    const int words = (min(q_tiles - walk0, WALK) + 63) >> 6;
+    // The list of those of the next WALK tiles that see a key of this block; bit 15:
+    // not all of its keys with all of their rows.
+    const int n = min(q_tiles - walk0, WALK), words = (n + 63) >> 6;
     __syncthreads();
-    for (int i = tid; i < words * 64; i += 256) {
-      const int qt = walk0 + i;
-      bool act = qt < q_tiles, part = false;
+    for (int i = tid; i < words * 64; i += 512) {
+      bool act = i < n;
       if (act && p.tile_spans) {
-        const int4 r = p.tile_spans[(int64_t)b * q_tiles + qt];
+        const int4 r = p.tile_spans[(int64_t)b * q_tiles + walk0 + i];
         act = r.x < key0 + 128 && r.y > key0;
-        part = r.z > key0 || r.w < min(key0 + 128, p.kv_len);
       }
-      const uint64_t a = __builtin_amdgcn_ballot_w64(act), c = __builtin_amdgcn_ballot_w64(part);
-      if (lane == 0) {
-        active[i >> 6] = a;
-        partial[i >> 6] = c;
-      }
+      const uint64_t a = __builtin_amdgcn_ballot_w64(act);
+      if (lane == 0) active[i >> 6] = a;
     }
     __syncthreads();
-    // This block's run of the (head, tile) pairs: `left` pairs from tile qt of
-    // head `head` on.
     int count = 0;
-    for (int w = 0; w < words; w++) count += __builtin_popcountll(active[w]);
+    for (int w = 0; w < words; w++) {
+      const uint64_t a = active[w];
+      if ((w & 7) == wave && a >> lane & 1) {
+        bool part = false;
+        if (p.tile_spans) {
+          const int4 r = p.tile_spans[(int64_t)b * q_tiles + walk0 + 64 * w + lane];
+          part = r.z > key0 || r.w < min(key0 + 128, p.kv_len);
+        }
+        list[count + __builtin_popcountll(a & ((1ull << lane) - 1))] =
+            (uint16_t)(64 * w + lane + (part ? 0x8000 : 0));
+      }
+      count += __builtin_popcountll(a);
+    }
     count = __builtin_amdgcn_readfirstlane(count);
+    __syncthreads();
+    // This block's run of the (head, tile) pairs: `left` of them from list[at] of
+    // head `head` on.
     const int64_t pairs = (int64_t)count * p.share;
     const int64_t from = pairs * piece / p.kv_parts;
     int left = (int)(pairs * (piece + 1) / p.kv_parts - from);
     if (left == 0) continue;
-    auto next = [&](int from) {  // the first active tile from `from` on, or -1
-      for (int w = from >> 6; w < words; w++) {
-        uint64_t m = active[w];
-        if (w == from >> 6) m &= ~0ull << (from & 63);
-        if (m) return __builtin_amdgcn_readfirstlane((w << 6) + __builtin_ctzll(m));
-      }
-      return -1;
-    };
-    const int first = next(0);
-    int head = kvh * p.share + (int)(from / count), qt = first;
-    if (from % count) {  // the active tile number from % count
-      int skip = (int)(from % count), w = 0;
-      uint64_t m = active[0];
-      for (; skip >= __builtin_popcountll(m); m = active[++w]) skip -= __builtin_popcountll(m);
-      for (; skip > 0; skip--) m &= m - 1;
-      qt = __builtin_amdgcn_readfirstlane((w << 6) + __builtin_ctzll(m));
-    }
+    int head = kvh * p.share + (int)(from / count), at = (int)(from % count);
+    auto tile_at = [&](int i) { return (int)__builtin_amdgcn_readfirstlane(list[i]); };
 
-    float lse = 0.0f, delta = 0.0f;
-    int2 span = make_int2(0, 0);
-    int row = 0;
-    using Tile = Copy<E, D, 256, KT>;
-    auto load = [&](int head, int qt, Buf &to) {  // the row values wait in registers for put()
-      const int t0 = (walk0 + qt) * KT;
+    // Queries, output gradients and row values of tile `t` of head `head`.
+    using Tile = Copy<E, D, 512, KT>;
+    auto load = [&](int t, Buf &to, int in) {
+      const int t0 = (walk0 + (t & 0x7fff)) * KT;
       Tile::issue({tok_row<E>(p.q, b, 0, head), p.q.ts, p.q_len, p.dim}, t0, to[0], tid);
       Tile::issue({tok_row<E>(p.d_o, b, 0, head), p.d_o.ts, p.q_len, p.dim}, t0, to[1], tid);
-      if (tid < KT) {
-        row = t0 + tid;
-        lse = -INFINITY;
-        delta = 0.0f;
-        span = make_int2(0, 0);
-        if (row < p.q_len) {
-          const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + row;
-          lse = p.lse[at];
-          delta = p.delta[at];
-          if (p.tile_spans) span = raw_span(p, b, row);
-        }
+      const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_pad + t0;
+      // (constant places: of one that depends on the wave the compiler would not see
+      // that it is none of the tiles')
+      if (wave == 0) copy_words(p.row_lse + at, stat[in][0], lane);
+      if (wave == 1) copy_words(p.row_delta + at, stat[in][1], lane);
+      if (wave < 4 || !p.tile_spans) return;
+      const int *spans_at = (const int *)(p.row_spans + (int64_t)b * p.q_pad + t0);
+      if (wave == 4) copy_words(spans_at, (int *)spans[in], lane);
+      if (wave == 5) copy_words(spans_at + 64, (int *)spans[in] + 64, lane);
+    };
+    // Steps to the next tile; `then` is the one after it, read from the list a turn
+    // before it is needed.
+    auto step = [&]() {
+      if (++at == count) {
+        at = 0;
+        head++;
       }
     };
-    auto put = [&](int at) {
-      if (tid < KT) {
-        // a row that sees nothing, or is past the end: p = 2^-inf = 0
-        stat[at][0][tid] = lse == -INFINITY
-                                    ? -INFINITY
-                                    : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
-        stat[at][1][tid] = -delta;
-        spans[at][tid] = cut_span(p, row, span);
+    int now = tile_at(at);
+    load(now, b0, 0);
+    step();
+    int next = tile_at(at);
+    // One tile, in buffer `here`; the next one is sent for into `there`.
+    auto turn = [&](Buf &here, Buf &there, int in) {
+      block_copied();  // this tile is there, and nobody reads the other one any more
+      const bool part = now & 0x8000;
+      const E *q = here[0], *g = here[1];
+      const int z = opaque_zero() + 32 * (wave & 3) * D;
+      // The operands of step k of both products, AHEAD steps before they are used.
+      constexpr int STEPS = D / 16, AHEAD = D == 64 ? 2 : 1;
+      frag<E> x[4][STEPS];
+      auto read = [&](int k) {
+        x[0][k] = lds_rows<E, D>(q, 32 * half, k, lane);
+        x[1][k] = lds_rows<E, D>(own_k + z, 0, k, lane);
+        x[2][k] = lds_rows<E, D>(g, 32 * half, k, lane);
+        x[3][k] = lds_rows<E, D>(own_v + z, 0, k, lane);
+      };
+      f32x16 w, ds;
+#pragma unroll
+      for (int k = 0; k < AHEAD; k++) read(k);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int r = 32 * half + acc_row(i, lane);
+        const f32x4 l4 = *(const f32x4 *)&stat[in][0][r];
+        const f32x4 d4 = *(const f32x4 *)&stat[in][1][r];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          w[i + c] = l4[c];
+          ds[i + c] = d4[c];
+        }
       }
-    };
-    auto after = [&](int &h, int &t) {  // the tile after tile t of head h
-      t = next(t + 1);
-      if (t < 0) {
-        t = first;
-        h++;
+      left--;
+      now = next;
+      if (left > 0) {
+        load(now, there, in ^ 1);
+        step();
+        next = tile_at(at);
       }
-    };
-    frag<E> rq[D / 16], rg[D / 16], cq[2][D / 32], cg[2][D / 32], pw[2], pd[2];
-    auto rows = [&](Buf &of, int row0) {
 #pragma unroll
-      for (int k = 0; k < D / 16; k++) {
-        rq[k] = lds_rows<E, D>(of[0], row0, k, lane);
-        rg[k] = lds_rows<E, D>(of[1], row0, k, lane);
-      }
-    };
-    auto add = [&]() {  // the last block into dK and dV
-#pragma unroll
-      for (int k = 0; k < 2; k++)
-#pragma unroll
-        for (int d = 0; d < D / 32; d++) {
-          dv[d] = mfma(cg[k][d], pw[k], dv[d]);
-          dk[d] = mfma(cq[k][d], pd[k], dk[d]);
-        }
-    };
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-      pw[k] = pd[k] = (E)0.0f;
-#pragma unroll
-      for (int d = 0; d < D / 32; d++) cq[k][d] = cg[k][d] = (E)0.0f;
-    }
-    auto sync = [&]() {  // the tile put last is there
-      copied<0>();
-      __syncthreads();
-    };
-
-    int nhead = head, nqt = qt;
-    load(head, qt, b0);
-    put(0);
-    sync();
-    after(nhead, nqt);
-    if (left > 1) load(nhead, nqt, b1);
-    rows(b0, 0);
-    // One tile, in buffer `at`; the next one goes to buffer `to`, the one after it
-    // to `then`.
-    auto turn = [&](Buf &here, Buf &there, Buf &then, int at, int to) {
-      const bool part = partial[qt >> 6] >> (qt & 63) & 1;
-#pragma unroll
-      for (int s = 0; s < KT / 32; s++) {
-        const bool last = s == KT / 32 - 1;
-        f32x16 w, ds;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int r = 32 * s + acc_row(i, lane);
-          const f32x4 l4 = *(const f32x4 *)&stat[at][0][r];
-          const f32x4 d4 = *(const f32x4 *)&stat[at][1][r];
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            w[i + c] = l4[c];
-            ds[i + c] = d4[c];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-          w = mfma(rq[k], kf[k], w);
-          ds = mfma(rg[k], vf[k], ds);
-        }
-        if (part) {
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int2 r = spans[at][32 * s + acc_row(i, lane)];
-            if ((unsigned)(key - r.x) >= (unsigned)(r.y - r.x)) {
-              w[i] = -INFINITY;
-              ds[i] = 0.0f;
-            }
-          }
-        }
-        if (last) {
-          // The next tile's values are put and its copies awaited; the one after it
-          // is sent for, into the buffer whose last reads came before this barrier in
-          // every wave.
-          if (left > 1) put(to);
-          sync();
-          qt = nqt;
-          left--;
-          after(nhead, nqt);
-          if (left > 1) load(nhead, nqt, then);
-        }
+      for (int k = 0; k < STEPS; k++) {
         __builtin_amdgcn_sched_barrier(0);
-        add();
+        if (k + AHEAD < STEPS) read(k + AHEAD);
+        w = mfma(x[0][k], x[1][k], w);
+        ds = mfma(x[2][k], x[3][k], ds);
+      }
+      frag<E> cols[2][D / 32];  // of dO, on their way while the vector unit works
+#pragma unroll
+      for (int d = 0; d < D / 32; d++) cols[0][d] = lds_cols<E, D, KT>(g, 32 * half, d, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      if (part) {
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-          w[i] = __builtin_amdgcn_exp2f(w[i] * p.scale_log2);
-          ds[i] *= w[i];
-          if (is_half<E>) ds[i] *= ds_by;
-        }
-        // past the last tile these are reads of what the buffer holds, for nothing
-        rows(last ? there : here, last ? 0 : 32 * (s + 1));
-        // In order: a matrix instruction, its share of the vector work and of the reads.
-        // A wave issues in order, and a matrix instruction holds it while the unit is
-        // busy: vector work placed behind all of them would wait for all of them.
-#pragma unroll
-        for (int i = 0; i < D / 8; i++) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // matrix
-          __builtin_amdgcn_sched_group_barrier(0x002, 3 * 128 / D, 0);    // vector
-          __builtin_amdgcn_sched_group_barrier(0x400, 128 / D, 0);        // exp
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);              // LDS read
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          pw[k] = pack8<E>(w, k);
-          pd[k] = pack8<E>(ds, k);
-#pragma unroll
-          for (int d = 0; d < D / 32; d++) {
-            cg[k][d] = lds_cols<E, D>(here[1], 32 * s + 16 * k, d, lane);
-            cq[k][d] = lds_cols<E, D>(here[0], 32 * s + 16 * k, d, lane);
+          const int2 r = spans[in][32 * half + acc_row(i, lane)];
+          if ((unsigned)(key - r.x) >= (unsigned)(r.y - r.x)) {
+            w[i] = -INFINITY;
+            ds[i] = 0.0f;
           }
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        w[i] = __builtin_amdgcn_exp2f(w[i] * p.scale_log2);
+        ds[i] *= w[i];
+        if (is_half<E>) ds[i] *= ds_by;
+      }
+      frag<E> pw[2], pd[2];
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        pw[k] = pack8<E>(w, k);
+        pd[k] = pack8<E>(ds, k);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // Groups of D / 32 transposed operands: dO and Q for the first 16 rows, then for
+      // the others, each read while the one before it is used.
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        if (c < 3)
+#pragma unroll
+          for (int d = 0; d < D / 32; d++)
+            cols[(c + 1) & 1][d] =
+                lds_cols<E, D, KT>(c & 1 ? g : q, 32 * half + (c ? 16 : 0), d, lane);
+#pragma unroll
+        for (int d = 0; d < D / 32; d++) {
+          if (c & 1) dk[d] = mfma(cols[1][d], pd[c >> 1], dk[d]);
+          else dv[d] = mfma(cols[0][d], pw[c >> 1], dv[d]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     while (left > 0) {
-      turn(b0, b1, b2, 0, 1);
-      if (left > 0) turn(b1, b2, b0, 1, 2);
-      if (left > 0) turn(b2, b0, b1, 2, 0);
+      turn(b0, b1, 0);
+      if (left > 0) turn(b1, b0, 1);
     }
-    add();
   }
+  copied<0>();
+
+  // The two halves' sums: the upper waves' through LDS to the lower ones.
+  float *sum = (float *)&b0;  // [128][D / 2 + 4], a half of the elements at a time
+#pragma unroll
+  for (int h = 0; h < 4; h++) {
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < D / 64; d++) {
+      f32x16 &x = h < 2 ? dk[(h & 1) * (D / 64) + d] : dv[(h & 1) * (D / 64) + d];
+      float *row = sum + (32 * (wave & 3) + (lane & 31)) * (D / 2 + 4) + 32 * d;
+      if (half)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *(f32x4 *)(row + acc_row(i, lane)) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < D / 64; d++) {
+      f32x16 &x = h < 2 ? dk[(h & 1) * (D / 64) + d] : dv[(h & 1) * (D / 64) + d];
+      const float *row = sum + (32 * (wave & 3) + (lane & 31)) * (D / 2 + 4) + 32 * d;
+      if (!half)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const f32x4 y = *(const f32x4 *)(row + acc_row(i, lane));
+#pragma unroll
+          for (int c = 0; c < 4; c++) x[i + c] += y[c];
+        }
+    }
+  }
+  if (half) return;
 
   const float by_k = is_half<E> ? ldexpf(p.scale, -e) : p.scale, by_v = is_half<E> ? 0x1p-15f : 1.0f;
   if (p.kv_parts > 1) {
@@ -534,7 +535,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
   __shared__ float tops[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int item = die_order(blockIdx.x, gridDim.x);
   const int piece = item % p.q_parts, whole = item / p.q_parts;
   const int2 at = block_item(p, whole, p.batch * p.q_heads, tiles);
@@ -543,7 +544,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
 
   float v_top = 0.0f;
   if (is_half<E>)
-    v_top = block_top(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, 1, tops);
+    v_top = block_top<256>(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, 1, tops);
   frag<E> q[NQ][D / 16], g[NQ][D / 16];
   int2 span[NQ];
   float lse[NQ], delta[NQ];
@@ -565,7 +566,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
       }
       const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
       lse[n] = p.lse[at];
-      delta[n] = p.delta[at];
+      delta[n] = -p.row_delta[(int64_t)bh * p.q_pad + t];
     }
     const E *qr = tok_row<E>(p.q, b, on ? t : 0, head), *gr = tok_row<E>(p.d_o, b, on ? t : 0, head);
     float norm = 0.0f;
@@ -741,7 +742,7 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
   if (err != hipSuccess) return err;
   const int k_tiles = (p.kv_len + 127) / 128, tiles = (p.q_len + 127) / 128;
   if (k_tiles) {
-    k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles * p.kv_parts, 256, 0, st>>>(p, k_tiles,
+    k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles * p.kv_parts, 512, 0, st>>>(p, k_tiles,
                                                                                     q_tiles);
     if (p.kv_parts > 1) {
       const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;

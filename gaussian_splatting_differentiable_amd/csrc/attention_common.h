@@ -138,6 +138,21 @@ struct Copy {
   }
 };
 
+// 0, which the compiler does not know: what is read from LDS at an offset of it in a
+// loop is read in every turn, not kept in registers across them.
+__device__ __forceinline__ int opaque_zero() {
+  int z;
+  asm volatile("s_mov_b32 %0, 0" : "=s"(z));
+  return z;
+}
+
+// One wave copies 64 words into LDS, as Copy does.
+template <class T>
+__device__ __forceinline__ void copy_words(const T *from, T *lds, int lane) {
+  auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, 256, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, lds), 4, lane * 4, 0, 0, 0);
+}
+
 // Waits until at most `left` of this wave's newest memory operations are under way
 // (0: all are done), and for its LDS reads.
 template <int left>
@@ -168,15 +183,20 @@ __device__ __forceinline__ frag<E> lds_rows(const E *tile, int row0, int k, int 
 
 // Operand A of the transpose: rows = elements 32 d .. + 31 of the tile's rows,
 // contraction = tile rows row0 .. + 15 (row0 a multiple of 16) in the order of a
-// score register run. The rows 8 further on have the swizzle of these ^ 2.
-template <class E, int D>
+// score register run. The rows 8 further on have the swizzle of these ^ 2. ROWS: the
+// tile's rows, where row0 is not known to the compiler; it must see that the reads
+// stay in their buffer, or they wait for copies into the others.
+template <class E, int D, int ROWS = 0>
 __device__ __forceinline__ frag<E> lds_cols(const E *tile, int row0, int d, int lane) {
   const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
   const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = 4 * (lane & 1);
-  const E *at = tile + row0 * D + in;
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, at + lds_at<D>(r, c)));
-  const i16x4 b =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, at + 8 * D + lds_at<D>(r, c ^ 2)));
+  int x = row0 * D + in + lds_at<D>(r, c), y = row0 * D + in + 8 * D + lds_at<D>(r, c ^ 2);
+  if (ROWS) {
+    x &= ROWS * D - 1;
+    y &= ROWS * D - 1;
+  }
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + x));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + y));
   return __builtin_bit_cast(frag<E>, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p
   using Buf = E[2][KT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int item = die_order(blockIdx.x, gridDim.x);
   const int2 bt = block_item(p, item, p.batch * p.q_heads, tiles);
   const int bh = bt.x, tile = bt.y, b = bh / p.q_heads, head = bh - b * p.q_heads;
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   using Buf = E[4][2][FT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ float ml[4][2][32];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int item = die_order(blockIdx.x, gridDim.x);
   const int part = item % p.splits, rest = item / p.splits;
   const int rt = rest % row_tiles, bh = rest / row_tiles;

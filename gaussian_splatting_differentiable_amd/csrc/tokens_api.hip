@@ -151,7 +151,10 @@ size_t attn_bwd_layout(AttnK *p, bool masked, bool half, void *ws) {
     total += round256(bytes);
     return r;
   };
-  p->delta = (float *)part(b * p->q_heads * p->q_len * 4);
+  p->q_pad = (int)(qt * 64);
+  p->row_lse = (float *)part(b * p->q_heads * p->q_pad * 4);
+  p->row_delta = (float *)part(b * p->q_heads * p->q_pad * 4);
+  p->row_spans = (int2 *)part(masked ? b * p->q_pad * 8 : 0);
   char *spans = part(masked ? b * qt * 16 : 0);
   p->tile_spans = masked ? (int4 *)spans : nullptr;
   p->q_bound = (float *)part(half ? b * p->q_heads * qt * 8 : 0);

@@ -93,7 +93,9 @@ struct AttnK {
   float *part_o, *part_ml;
   // backward
   TokK d_o, dq, dk, dv;
-  float *delta;
+  int q_pad;  // queries, rounded up to whole tiles of 64
+  float *row_lse, *row_delta;  // [batch][q_heads][q_pad]: -lse / scale (fp16: less 15 bits), -D_i
+  int2 *row_spans;             // [batch][q_pad]: spans as the masks leave them
   int4 *tile_spans;
   float *q_bound, *v_bound;
   int q_parts, kv_parts;
