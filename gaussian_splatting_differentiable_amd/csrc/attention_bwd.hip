@@ -4,9 +4,9 @@
 //   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
 // the sums over i also over the heads that share key j.
 //
-// Three launches: D (and what the others need to skip tiles), then dK and dV by
+// The launches: D (and what the others need to skip tiles), then dK and dV by
 // blocks that own keys and stream queries, then dQ by blocks that own queries and
-// stream keys. The scores are computed in both (7 products of the size of
+// stream keys, then the sums of what was computed in parts. The scores are computed in both (7 products of the size of
 // q . k^T instead of 5): in exchange no sum is made by atomics, so results do not
 // depend on timing, and nothing of size q_len x kv_len is ever stored.
 //
@@ -115,6 +115,40 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int lane) {
 // for each 64 queries the keys that some row sees and that all see (lo, hi, in_lo,
 // in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
 // largest |v_j| of each 64 keys. 16 lanes a row.
+//
+// o was rounded to 16 bits, and D_i of it is off by as much. Beside gradients of many
+// keys that is little, but rows of a few have the largest ones: their D_i are summed
+// from their pairs, sum_j p_ij (do_i . v_j). Relative error of dq, causal, bf16, 64
+// queries: 0.0030 with o alone, 0.0025 so (0.0023 with exact D_i: ds in 16 bits). Of 16
+// keys it is 0.0024 and costs twice as much: 8 us instead of 4 of 4096 causal queries'
+// 720, a chain of loads that the few blocks with such rows wait for.
+constexpr int D_PAIRS = 8;
+
+template <class E>
+__device__ __forceinline__ float pairs_d(const AttnK &p, int b, int head, int t, int2 see,
+                                         int j) {
+  const int kvh = head / p.share;
+  const float lse = p.lse[((int64_t)b * p.q_heads + head) * p.q_len + t] * ATTN_LOG2E;
+  const bool in = 8 * j < p.dim;
+  const int at = in ? 8 * j : 0;
+  const E *q = tok_row<E>(p.q, b, t, head) + at, *g = tok_row<E>(p.d_o, b, t, head) + at;
+  const frag<E> fq = *(const frag<E> *)q, fg = *(const frag<E> *)g;
+  float d = 0.0f;
+  for (int key = see.x; key < see.y; key++) {
+    const frag<E> k = *(const frag<E> *)(tok_row<E>(p.k, b, key, kvh) + at);
+    const frag<E> v = *(const frag<E> *)(tok_row<E>(p.v, b, key, kvh) + at);
+    float s = 0.0f, dp = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      s = fmaf((float)fq[e], (float)k[e], s);
+      dp = fmaf((float)fg[e], (float)v[e], dp);
+    }
+    s = group_sum(in ? s : 0.0f, 16) * p.scale_log2 - lse;
+    d = fmaf(__builtin_amdgcn_exp2f(s), group_sum(in ? dp : 0.0f, 16), d);
+  }
+  return d;
+}
+
 template <class E>
 __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_tiles) {
   __shared__ float top[4][2];
@@ -133,6 +167,7 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
       if (lane == 0) p.tile_spans[(int64_t)b * q_tiles + qt] = r;
       p.row_spans[(int64_t)b * p.q_pad + t] = s;
     }
+    int few = 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int t = qt * KT + 16 * i + (tid >> 4);
@@ -148,10 +183,13 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
         }
       }
       d = group_sum(d, 16);
+      const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
+      const int2 see = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
+      const bool pairs = see.x < see.y && see.y - see.x <= D_PAIRS;
+      few |= (int)pairs << i;
       if (j == 0) {
         const int64_t at = (int64_t)bh * p.q_pad + t;
-        const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
-        p.row_delta[at] = -d;
+        if (!pairs) p.row_delta[at] = -d;
         p.row_lse[at] = lse == -INFINITY
                             ? -INFINITY
                             : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
@@ -160,6 +198,15 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
         m0 = fmaxf(m0, sqrtf(group_sum(n, 16)));
         m1 = fmaxf(m1, fabsf(d));
       }
+    }
+    // a loop of its own, not unrolled: registers for one row's pairs, not for four
+#pragma unroll 1
+    for (int i = 0; i < 4; i++) {
+      if (!(few >> i & 1)) continue;
+      const int t = qt * KT + 16 * i + (tid >> 4);
+      const float d = pairs_d<E>(p, b, head, t, row_span(p, b, t), j);
+      if (j == 0) p.row_delta[(int64_t)bh * p.q_pad + t] = -d;
+      m1 = fmaxf(m1, fabsf(d));
     }
   } else {
     const int at = blockIdx.x - q_blocks, bh = at / kv_tiles, jt = at - bh * kv_tiles;
@@ -258,9 +305,12 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[D / 32], float by
 // see them in tiles of 64, head after head of those that share the key head: wave w
 // takes keys 32 (w % 4) .. + 31 and rows 32 (w / 4) .. + 31 of every tile, so that
 // each SIMD has two waves whose matrix and vector work overlap. K and V stay in LDS
-// (beside dK and dV a wave's 256 registers have no room for them). Where there are too few such blocks, or masks make them uneven, a block takes
-// one of kv_parts equal runs of those tiles, and k_attn_sum adds the parts' 32-bit
-// sums. -lse / scale and -D_i are the accumulators' starting values.
+// (beside dK and dV a wave's 256 registers have no room for them). Where there are too
+// few such blocks, or masks make them uneven, a block takes one of kv_parts equal runs
+// of those tiles, and k_attn_sum adds the parts' 32-bit sums. -lse / scale and -D_i are
+// the accumulators' starting values. Bound by the matrix units: 16384 tokens, 8 heads of
+// 128 on 2, bf16: 1990 us, 1105 TFLOP/s of its four products (four waves a block, 32
+// keys each and all rows: 2350 us).
 template <class E, int D>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
                                                                        int q_tiles) {
@@ -527,65 +577,56 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
 
 // ------------------------------------------------------------ dQ
 // The forward's walk with a second score product and without a running maximum; a
-// block takes one of q_parts runs of its key tiles, as above.
-template <class E, int D, int NQ>
-__global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK p, int tiles,
-                                                                            int kv_tiles) {
+// block takes one of q_parts runs of its key tiles, as above. Bound by the matrix
+// units' rate at the clock that their power leaves: 16384 tokens, 8 heads of 128, bf16:
+// 1370 us, 1200 TFLOP/s of its three products. Heads of 65 to 96 have a form of 96 (2 x 2048 queries,
+// 12 heads of 80, bf16: 74 us, in the form of 128 90).
+template <class E, int D>
+__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int kv_tiles) {
   using Buf = E[2][KT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
   __shared__ float tops[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int item = die_order(blockIdx.x, gridDim.x);
-  const int piece = item % p.q_parts, whole = item / p.q_parts;
-  const int2 at = block_item(p, whole, p.batch * p.q_heads, tiles);
-  const int bh = at.x, tile = at.y, b = bh / p.q_heads, head = bh - b * p.q_heads;
-  const int kvh = head / p.share, row0 = tile * 128 * NQ + wave * 32 * NQ + (lane & 31);
+  const int once = gridDim.x / p.passes, pass = blockIdx.x / once;
+  const int run = die_order(blockIdx.x % once, once);
+  const int piece = run % p.q_parts, whole = run / p.q_parts;
+  const int2 bt = block_item(p, whole, p.batch * p.q_heads, tiles);
+  const int bh = bt.x, tile0 = bt.y * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
+  const int kvh = head / p.share, t = tile0 + wave * 32 + (lane & 31);
+  bool on = t < p.q_len;
+  int2 span = on ? row_span(p, b, t) : make_int2(0, 0);
+  if (p.passes == 2) {
+    const bool other = apart(span, range, wave, lane);  // every thread: it has a barrier
+    on = on && other == (pass == 1);
+    if (!on) span = make_int2(0, 0);
+    if (__syncthreads_count(on) == 0) return;
+  }
 
   float v_top = 0.0f;
   if (is_half<E>)
     v_top = block_top<256>(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, 1, tops);
-  frag<E> q[NQ][D / 16], g[NQ][D / 16];
-  int2 span[NQ];
-  float lse[NQ], delta[NQ];
-  int e[NQ];
-  int lo = INT32_MAX, hi = 0, in_lo = 0, in_hi = INT32_MAX;
+  const float row_lse = on ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
+  const float delta = on ? -p.row_delta[(int64_t)bh * p.q_pad + t] : 0.0f;
+  frag<E> q[D / 16], g[D / 16];
+  const E *qr = tok_row<E>(p.q, b, on ? t : 0, head), *gr = tok_row<E>(p.d_o, b, on ? t : 0, head);
+  float norm = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NQ; n++) {
-    const int t = row0 + 32 * n;
-    const bool on = t < p.q_len;
-    span[n] = on ? row_span(p, b, t) : make_int2(0, 0);
-    lse[n] = -INFINITY;
-    delta[n] = 0.0f;
-    if (on) {
-      in_lo = max(in_lo, span[n].x);
-      in_hi = min(in_hi, span[n].y);
-      if (span[n].x < span[n].y) {
-        lo = min(lo, span[n].x);
-        hi = max(hi, span[n].y);
-      }
-      const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
-      lse[n] = p.lse[at];
-      delta[n] = -p.row_delta[(int64_t)bh * p.q_pad + t];
-    }
-    const E *qr = tok_row<E>(p.q, b, on ? t : 0, head), *gr = tok_row<E>(p.d_o, b, on ? t : 0, head);
-    float norm = 0.0f;
+  for (int k = 0; k < D / 16; k++) {
+    const int chunk = 2 * k + (lane >> 5);
+    q[k] = row_operand<E>(qr, chunk, on && 8 * chunk < p.dim);
+    g[k] = row_operand<E>(gr, chunk, on && 8 * chunk < p.dim);
+    if (is_half<E>)
 #pragma unroll
-    for (int k = 0; k < D / 16; k++) {
-      const int chunk = 2 * k + (lane >> 5);
-      q[n][k] = row_operand<E>(qr, chunk, on && 8 * chunk < p.dim);
-      g[n][k] = row_operand<E>(gr, chunk, on && 8 * chunk < p.dim);
-      if (is_half<E>)
-#pragma unroll
-        for (int i = 0; i < 8; i++) norm = fmaf((float)g[n][k][i], (float)g[n][k][i], norm);
-    }
-    e[n] = is_half<E> ? headroom(sqrtf(other_half(norm, false)) * v_top + fabsf(delta[n])) : 0;
-    lse[n] = lse[n] == -INFINITY ? INFINITY : lse[n] * ATTN_LOG2E - (float)e[n];
+      for (int i = 0; i < 8; i++) norm = fmaf((float)g[k][i], (float)g[k][i], norm);
   }
-  lo = __builtin_amdgcn_readfirstlane(wave_min(lo));
-  hi = __builtin_amdgcn_readfirstlane(wave_max(hi));
-  in_lo = __builtin_amdgcn_readfirstlane(wave_max(in_lo));
-  in_hi = __builtin_amdgcn_readfirstlane(wave_min(in_hi));
+  const int e = is_half<E> ? headroom(sqrtf(other_half(norm, false)) * v_top + fabsf(delta)) : 0;
+  const float lse = row_lse == -INFINITY ? INFINITY : row_lse * ATTN_LOG2E - (float)e;
+  const bool some = span.x < span.y;
+  const int lo = __builtin_amdgcn_readfirstlane(wave_min(some ? span.x : INT32_MAX));
+  const int hi = __builtin_amdgcn_readfirstlane(wave_max(span.y));
+  const int in_lo = __builtin_amdgcn_readfirstlane(wave_max(on ? span.x : 0));
+  const int in_hi = __builtin_amdgcn_readfirstlane(wave_min(on ? span.y : INT32_MAX));
   if (lane == 0) range[wave] = make_int2(lo, hi);
   __syncthreads();
   int first = INT32_MAX, end = 0;
@@ -604,11 +645,9 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
 
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
-  f32x16 dq[NQ][D / 32];
+  f32x16 dq[D / 32];
 #pragma unroll
-  for (int n = 0; n < NQ; n++)
-#pragma unroll
-    for (int d = 0; d < D / 32; d++) dq[n][d] = 0.0f;
+  for (int d = 0; d < D / 32; d++) dq[d] = 0.0f;
   using Tile = Copy<E, D, 256, KT>;
   if (first < end) {
     Tile::issue(ks, first * KT, b0[0], tid);
@@ -626,21 +665,19 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
     const E *kt = here[0], *vt = here[1];
 #pragma unroll
     for (int s = 0; s < KT / 32; s++) {
-      f32x16 w[NQ], ds[NQ];
-      frag<E> a[D / 16], c[D / 16];
+      // The first product's operands are read together; the second one's arrive under
+      // it. Reads of both a few steps ahead of each use measured the same with heads of
+      // 64, and spill with heads of 128.
+      constexpr int STEPS = D / 16;
+      frag<E> a[STEPS];
 #pragma unroll
-      for (int k = 0; k < D / 16; k++) a[k] = lds_rows<E, D>(kt, 32 * s, k, lane);
+      for (int k = 0; k < STEPS; k++) a[k] = lds_rows<E, D>(kt, 32 * s, k, lane);
       __builtin_amdgcn_sched_barrier(0);
+      f32x16 w = 0.0f, ds = 0.0f;
 #pragma unroll
-      for (int k = 0; k < D / 16; k++) c[k] = lds_rows<E, D>(vt, 32 * s, k, lane);
+      for (int k = 0; k < STEPS; k++) w = mfma(a[k], q[k], w);
 #pragma unroll
-      for (int n = 0; n < NQ; n++) {
-        w[n] = ds[n] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) w[n] = mfma(a[k], q[n][k], w[n]);
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) ds[n] = mfma(c[k], g[n][k], ds[n]);
-      }
+      for (int k = 0; k < STEPS; k++) ds = mfma(lds_rows<E, D>(vt, 32 * s, k, lane), g[k], ds);
       frag<E> cols[2][D / 32];  // on their way while the vector unit works
 #pragma unroll
       for (int k = 0; k < 2; k++)
@@ -648,24 +685,20 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
         for (int d = 0; d < D / 32; d++) cols[k][d] = lds_cols<E, D>(kt, 32 * s + 16 * k, d, lane);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NQ; n++) {
+      for (int i = 0; i < 16; i++)
+        ds[i] = __builtin_amdgcn_exp2f(fmaf(w[i], p.scale_log2, -lse)) * (ds[i] - delta);
+      if (!full) {
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-          ds[n][i] = __builtin_amdgcn_exp2f(fmaf(w[n][i], p.scale_log2, -lse[n])) *
-                     (ds[n][i] - delta[n]);
-        if (!full) {
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int key = key0 + 32 * s + acc_row(i, lane);
-            if ((unsigned)(key - span[n].x) >= (unsigned)(span[n].y - span[n].x)) ds[n][i] = 0.0f;
-          }
+        for (int i = 0; i < 16; i++) {
+          const int key = key0 + 32 * s + acc_row(i, lane);
+          if ((unsigned)(key - span.x) >= (unsigned)(span.y - span.x)) ds[i] = 0.0f;
         }
+      }
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const frag<E> pd = pack8<E>(ds[n], k);
+      for (int k = 0; k < 2; k++) {
+        const frag<E> pd = pack8<E>(ds, k);
 #pragma unroll
-          for (int d = 0; d < D / 32; d++) dq[n][d] = mfma(cols[k][d], pd, dq[n][d]);
-        }
+        for (int d = 0; d < D / 32; d++) dq[d] = mfma(cols[k][d], pd, dq[d]);
       }
     }
   };
@@ -673,36 +706,33 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_bwd_q(AttnK
     turn(j, b0, b1);
     if (j + 1 < end) turn(j + 1, b1, b0);
   }
-#pragma unroll
-  for (int n = 0; n < NQ; n++) {
-    const int t = row0 + 32 * n;
-    const bool on = t < p.q_len;
-    const float by = is_half<E> ? ldexpf(p.scale, -e[n]) : p.scale;
-    if (p.q_parts > 1) {
-      const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
-      store_part<D>(dq[n], by, p.part_q + (piece * rows + (int64_t)bh * p.q_len + t) * p.dim, on,
-                    p.dim, lane);
-      continue;
-    }
-    uint32_t again = store_rows<E, D>(dq[n], by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim,
-                                      lane, 0);
-    while (again) {
-      const int r = __builtin_ctz(again);
-      again &= again - 1;
-      redo_query<E>(p, b, head, tile * 128 * NQ + wave * 32 * NQ + 32 * n + r, lane);
-    }
+
+  const float by = is_half<E> ? ldexpf(p.scale, -e) : p.scale;
+  if (p.q_parts > 1) {
+    const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
+    store_part<D>(dq, by, p.part_q + (piece * rows + (int64_t)bh * p.q_len + t) * p.dim, on, p.dim,
+                  lane);
+    return;
+  }
+  uint32_t again =
+      store_rows<E, D>(dq, by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim, lane, 0);
+  if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
+  while (again) {
+    const int r = __builtin_ctz(again);
+    again &= again - 1;
+    redo_query<E>(p, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
 // ------------------------------------------------------------ the parts' sums
 // 32 lanes a row, in the order of the parts: rows of dQ (KEYS 0), or of dK and dV.
 template <class E, bool KEYS>
-__global__ __launch_bounds__(256) void k_attn_sum(AttnK p) {
+__device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
   const int lane = threadIdx.x & 63, e = 4 * (lane & 31);
   const int len = KEYS ? p.kv_len : p.q_len, heads = KEYS ? p.kv_heads : p.q_heads;
   const int parts = KEYS ? p.kv_parts : p.q_parts;
   const int64_t rows = (int64_t)p.batch * heads * len;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)block * 8 + (threadIdx.x >> 5);
   const bool on = row < rows && e < p.dim;
   const int64_t bh = (on ? row : 0) / len;
   const int t = (int)((on ? row : 0) - bh * len), b = (int)(bh / heads);
@@ -733,6 +763,13 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnK p) {
   }
 }
 
+// Both in one launch, a block of 8 rows of either: the first `key_blocks` are keys'.
+template <class E>
+__global__ __launch_bounds__(256) void k_attn_sum(AttnK p, int key_blocks) {
+  if ((int)blockIdx.x < key_blocks) sum_rows<E, true>(p, blockIdx.x);
+  else sum_rows<E, false>(p, blockIdx.x - key_blocks);
+}
+
 template <class E, int D>
 hipError_t launch(const AttnK &p, hipStream_t st) {
   const int q_tiles = (p.q_len + KT - 1) / KT, kv_tiles = (p.kv_len + KT - 1) / KT;
@@ -744,21 +781,20 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
   if (k_tiles) {
     k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles * p.kv_parts, 512, 0, st>>>(p, k_tiles,
                                                                                     q_tiles);
-    if (p.kv_parts > 1) {
-      const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;
-      k_attn_sum<E, true><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-    }
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   if (tiles) {
-    k_attn_bwd_q<E, D, 1><<<p.batch * p.q_heads * tiles * p.q_parts, 256, 0, st>>>(p, tiles,
-                                                                                   kv_tiles);
-    if (p.q_parts > 1) {
-      const int64_t rows = (int64_t)p.batch * p.q_heads * p.q_len;
-      k_attn_sum<E, false><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-    }
+    const int blocks = p.batch * p.q_heads * tiles * p.q_parts * p.passes;
+    if (D == 128 && p.dim <= 96) k_attn_bwd_q<E, 96><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
+    else k_attn_bwd_q<E, D><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
+  auto blocks_of = [](int64_t rows, int parts) { return parts > 1 ? (int)((rows + 7) / 8) : 0; };
+  const int keys = blocks_of((int64_t)p.batch * p.kv_heads * p.kv_len, p.kv_parts);
+  const int queries = blocks_of((int64_t)p.batch * p.q_heads * p.q_len, p.q_parts);
+  if (keys + queries) k_attn_sum<E><<<keys + queries, 256, 0, st>>>(p, keys);
   return hipGetLastError();
 }
 
@@ -768,9 +804,10 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
 // compute units, at least two where masks make the blocks uneven and they are no
 // more than one for each, every part with four tiles or more. A part costs the
 // write and the read of its 32-bit sums.
-// Measured, q_len 2331, 8 heads of 64 (152 blocks), dK and dV with their sum: one
-// part 57 us, two 44, four 45; causal, 2 x 4096 queries, 16 heads of 128 on 4 (256
-// blocks): one 576, two 395.
+// Measured, q_len 2331, 8 heads of 64 (152 blocks): dK and dV in one part 55 us, in two
+// 38 and their sum 7, in four 49 and 8; dQ in one part 35, in two 24 and their sum 5;
+// causal, 2 x 4096 queries, 16 heads of 128 on 4 (256 blocks), dK and dV: in one part
+// 576, in two 328 and their sum 15.
 void gs_attn_bwd_plan(AttnK *p, bool masked) {
   auto parts = [masked](int64_t blocks, int64_t tiles) {
     int64_t n = blocks ? (256 + blocks - 1) / blocks : 1;
@@ -784,7 +821,10 @@ void gs_attn_bwd_plan(AttnK *p, bool masked) {
                      (p->kv_len + 63) / 64);
 }
 
-hipError_t gs_launch_attn_bwd(const AttnK &p, int dtype, hipStream_t st) {
+int gs_attn_passes(const AttnK &p);
+
+hipError_t gs_launch_attn_bwd(AttnK p, int dtype, hipStream_t st) {
+  p.passes = gs_attn_passes(p);
   if (dtype == GS_BF16) return p.dim <= 64 ? launch<bf16_t, 64>(p, st) : launch<bf16_t, 128>(p, st);
   return p.dim <= 64 ? launch<f16_t, 64>(p, st) : launch<f16_t, 128>(p, st);
 }

@@ -72,6 +72,24 @@ __device__ __forceinline__ int2 row_span(const AttnK &p, int b, int t) {
   return cut_span(p, t, raw_span(p, b, t));
 }
 
+// Rows of a 128-row block whose spans have no key in common with that of its first row
+// that sees any. A block whose rows belong to two sequences would walk over the keys
+// of both, one after the other; with p.passes 2 every block is launched twice, once
+// for the other rows and once for these (most of the second ones have none and end at
+// once). `firsts`: LDS for four spans; every thread of the block calls it.
+__device__ __forceinline__ bool apart(int2 span, int2 *firsts, int wave, int lane) {
+  const uint64_t some = __builtin_amdgcn_ballot_w64(span.x < span.y);
+  const int at = some ? __builtin_ctzll(some) : 0;
+  const int2 first = make_int2(__shfl(span.x, at), __shfl(span.y, at));
+  if (lane == 0) firsts[wave] = first;
+  __syncthreads();
+  int2 s = firsts[0];
+#pragma unroll
+  for (int w = 1; w < 4; w++)
+    if (s.x >= s.y) s = firsts[w];
+  return span.x < span.y && (span.x >= s.y || span.y <= s.x);
+}
+
 // Workgroups are dealt to the 8 dies in turn, each with an L2 of its own: give a
 // die a run of consecutive items, which share their heads' streamed rows.
 __device__ __forceinline__ int die_order(int block, int blocks) {
@@ -96,6 +114,7 @@ __device__ __forceinline__ int2 block_item(const AttnK &p, int item, int heads, 
 template <int D>
 __device__ __forceinline__ int swizzle(int row) {
   if (D == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  if (D == 96) return (row >> 2) & 3;  // a row is 3/4 of the banks: its 4 next ones differ
   return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);  // D == 64: two rows to the banks
 }
 
@@ -121,6 +140,7 @@ struct Stream {
 template <class E, int D, int NT, int R>
 struct Copy {
   static constexpr int C = D / 8, N = R * C / NT;
+  static_assert(R * C % NT == 0, "whole copies");
 
   static __device__ __forceinline__ void issue(const Stream<E> &m, int row0, E *lds, int tid) {
     const int left = min(m.rows - row0, R);
@@ -129,7 +149,8 @@ struct Copy {
                                                   (int)bytes, 0x00020000);
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int row = i * (NT / C) + tid / C, col = (tid % C) ^ swizzle<D>(row);
+      const int row = NT % C ? (i * NT + tid) / C : i * (NT / C) + tid / C;
+      const int col = (NT % C ? (i * NT + tid) % C : tid % C) ^ swizzle<D>(row);
       // past `dim`: an offset out of every tile's bounds
       const unsigned at = 8 * col < m.dim ? (unsigned)(row * (int)m.ts + 8 * col) * 2u : 0x7fffff00u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -190,13 +211,16 @@ template <class E, int D, int ROWS = 0>
 __device__ __forceinline__ frag<E> lds_cols(const E *tile, int row0, int d, int lane) {
   const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
   const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = 4 * (lane & 1);
-  int x = row0 * D + in + lds_at<D>(r, c), y = row0 * D + in + 8 * D + lds_at<D>(r, c ^ 2);
+  int x = in + lds_at<D>(r, c), y = in + lds_at<D>(r, c ^ 2), more = row0 * D;
   if (ROWS) {
-    x &= ROWS * D - 1;
-    y &= ROWS * D - 1;
+    x = (x + more) & (ROWS * D - 1);
+    y = (y + more) & (ROWS * D - 1);
+    more = 0;
   }
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + x));
-  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + y));
+  // The constant last: it stays in the instruction, and the lane's part in registers
+  // that all reads share.
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + x + more));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, tile + y + more + 8 * D));
   return __builtin_bit_cast(frag<E>, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 

@@ -51,90 +51,87 @@ __device__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
         l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
 }
 
-// A wave's running softmax over NQ blocks of 32 rows and its share of o.
-template <class E, int D, int NQ>
+// A wave's running softmax over its 32 rows and its share of o.
+template <class E, int D>
 struct Softmax {
-  f32x16 o[NQ][D / 32];
-  float m[NQ], l[NQ];
+  f32x16 o[D / 32];
+  float m, l;
 
   __device__ __forceinline__ void init() {
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NQ; n++) {
-      m[n] = -INFINITY;
-      l[n] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < D / 32; d++) o[n][d] = 0.0f;
-    }
+    for (int d = 0; d < D / 32; d++) o[d] = 0.0f;
   }
 
-  // One tile of 32 NS keys from row `key0` of the streams (row 0 of the tiles).
-  // full: every row of the wave sees all of them.
+  // A tile of 32 NS keys, the first of them `key0`. full: every row of the wave sees all
+  // of them.
   template <int NS>
-  __device__ __forceinline__ void tile(const E *kt, const E *vt, const frag<E> (&q)[NQ][D / 16],
-                                       const int2 (&span)[NQ], bool full, int key0,
-                                       float scale_log2, int lane) {
-    f32x16 s[NQ][NS];
-    frag<E> a[NS][D / 16];
-#pragma unroll
-    for (int k = 0; k < D / 16; k++)
+  __device__ __forceinline__ void tile(const E *kt, const E *vt, const frag<E> (&q)[D / 16],
+                                       int2 span, bool full, int key0, float scale_log2, int lane) {
+    // The keys' operands of step k, AHEAD steps before they are used: a wave waits for
+    // LDS once, not at every step, and the registers hold them beside o (168 of the form
+    // of 96, else 256; that one also reads no values early).
+    constexpr int STEPS = D / 16, AHEAD = D == 96 ? 2 : 4;
+    f32x16 s[NS];
+    frag<E> a[NS][STEPS];
+    auto read = [&](int k) {
 #pragma unroll
       for (int b = 0; b < NS; b++) a[b][k] = lds_rows<E, D>(kt, 32 * b, k, lane);
-    __builtin_amdgcn_sched_barrier(0);
+    };
 #pragma unroll
-    for (int k = 0; k < D / 16; k++)
+    for (int k = 0; k < AHEAD; k++) read(k);
 #pragma unroll
-      for (int n = 0; n < NQ; n++)
+    for (int k = 0; k < STEPS; k++) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + AHEAD < STEPS) read(k + AHEAD);
 #pragma unroll
-        for (int b = 0; b < NS; b++) {
-          if (k == 0) s[n][b] = 0.0f;
-          s[n][b] = mfma(a[b][k], q[n][k], s[n][b]);
-        }
-    if (!full) {
-#pragma unroll
-      for (int n = 0; n < NQ; n++)
-#pragma unroll
-        for (int b = 0; b < NS; b++)
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int j = key0 + 32 * b + acc_row(i, lane);
-            if ((unsigned)(j - span[n].x) >= (unsigned)(span[n].y - span[n].x))
-              s[n][b][i] = -INFINITY;
-          }
-    }
-    // the first half's values, on their way while the softmax is computed
-    frag<E> v0[2][D / 32];
-#pragma unroll
-    for (int k = 0; k < 2; k++)
-#pragma unroll
-      for (int d = 0; d < D / 32; d++) v0[k][d] = lds_cols<E, D>(vt, 16 * k, d, lane);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < NQ; n++) {
-      float top = s[n][0][0];
-#pragma unroll
-      for (int b = 0; b < NS; b++)
-#pragma unroll
-        for (int i = 0; i < 16; i++) top = fmaxf(top, s[n][b][i]);
-      top = other_half(top, true) * scale_log2;
-      if (__builtin_amdgcn_ballot_w64(top > m[n] + 8.0f)) {
-        const float to = fmaxf(m[n], top), ref = to == -INFINITY ? 0.0f : to;
-        const float shrink = __builtin_amdgcn_exp2f((m[n] == -INFINITY ? ref : m[n]) - ref);
-        m[n] = to;
-        l[n] *= shrink;
-#pragma unroll
-        for (int d = 0; d < D / 32; d++) o[n][d] *= shrink;
+      for (int b = 0; b < NS; b++) {
+        if (k == 0) s[b] = 0.0f;
+        s[b] = mfma(a[b][k], q[k], s[b]);
       }
-      const float ref = m[n] == -INFINITY ? 0.0f : m[n];
-      float sum = 0.0f;
+    }
+    if (!full) {
 #pragma unroll
       for (int b = 0; b < NS; b++)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-          s[n][b][i] = __builtin_amdgcn_exp2f(fmaf(s[n][b][i], scale_log2, -ref));
-          sum += s[n][b][i];
+          const int j = key0 + 32 * b + acc_row(i, lane);
+          if ((unsigned)(j - span.x) >= (unsigned)(span.y - span.x)) s[b][i] = -INFINITY;
         }
-      l[n] += sum;
     }
+    // the first 32 keys' values, on their way while the softmax is computed
+    frag<E> v0[2][D / 32];
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+#pragma unroll
+      for (int d = 0; d < D / 32; d++)
+        if (D != 96) v0[k][d] = lds_cols<E, D>(vt, 16 * k, d, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NS; b++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][i]);
+    top = other_half(top, true) * scale_log2;
+    if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+      const float to = fmaxf(m, top), ref = to == -INFINITY ? 0.0f : to;
+      const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
+      m = to;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < D / 32; d++) o[d] *= shrink;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NS; b++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], scale_log2, -ref));
+        sum += s[b][i];
+      }
+    l += sum;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < NS; b++) {
@@ -142,63 +139,64 @@ struct Softmax {
 #pragma unroll
       for (int k = 0; k < 2; k++)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++) c[k][d] = b ? lds_cols<E, D>(vt, 32 * b + 16 * k, d, lane) : v0[k][d];
+        for (int d = 0; d < D / 32; d++)
+          c[k][d] = b || D == 96 ? lds_cols<E, D>(vt, 32 * b + 16 * k, d, lane) : v0[k][d];
 #pragma unroll
-      for (int k = 0; k < 2; k++)
+      for (int k = 0; k < 2; k++) {
+        const frag<E> w = pack8<E>(s[b], k);
 #pragma unroll
-        for (int n = 0; n < NQ; n++) {
-          const frag<E> w = pack8<E>(s[n][b], k);
-#pragma unroll
-          for (int d = 0; d < D / 32; d++) o[n][d] = mfma(c[k][d], w, o[n][d]);
-        }
+        for (int d = 0; d < D / 32; d++) o[d] = mfma(c[k][d], w, o[d]);
+      }
     }
   }
 };
 
 // ------------------------------------------------------------ many rows
-// A block of four waves takes 128 NQ queries of one head and streams the keys
-// and values of their spans through LDS in tiles of 64, the next one on its way
-// while this one is computed.
-template <class E, int D, int NQ>
-__global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p, int tiles) {
+// A block takes 128 queries of one head, 32 a wave, and streams the keys and values
+// of their spans through LDS in tiles of 64, the next one on its way while this one is
+// computed.
+// Bound by the matrix units, and in short calls by how evenly blocks fall on the
+// compute units: 16384 tokens, 8 heads of 128, bf16: 1010 us, 1090 TFLOP/s. Heads of 65
+// to 96 have a form of 96, of which three blocks fit a compute unit: 6037 tokens in four
+// sequences, 12 heads of 80: 58 us, in the form of 128 73; 2 x 2048 tokens, 12 heads of
+// 80: 61 and 70. 64 rows a wave instead of 32 were slower: 2 x 8192 tokens, 16 heads of
+// 64: 808 us, with 32 690 (the exponentials of heads of 64 take as long as the products).
+template <class E, int D>
+__global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
   // sees that reads of one do not wait for copies into the other.
   using Buf = E[2][KT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int item = die_order(blockIdx.x, gridDim.x);
+  const int once = gridDim.x / p.passes, pass = blockIdx.x / once;
+  const int item = die_order(blockIdx.x % once, once);
   const int2 bt = block_item(p, item, p.batch * p.q_heads, tiles);
-  const int bh = bt.x, tile = bt.y, b = bh / p.q_heads, head = bh - b * p.q_heads;
-  const int kvh = head / p.share, row0 = tile * 128 * NQ + wave * 32 * NQ + (lane & 31);
+  const int bh = bt.x, tile0 = bt.y * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
+  const int kvh = head / p.share, t = tile0 + wave * 32 + (lane & 31);
+  bool on = t < p.q_len;
+  int2 span = on ? row_span(p, b, t) : make_int2(0, 0);
+  if (p.passes == 2) {
+    const bool other = apart(span, range, wave, lane);  // every thread: it has a barrier
+    on = on && other == (pass == 1);
+    if (!on) span = make_int2(0, 0);
+    if (__syncthreads_count(on) == 0) return;
+  }
 
-  frag<E> q[NQ][D / 16];
-  int2 span[NQ];
-  int lo = INT32_MAX, hi = 0, in_lo = 0, in_hi = INT32_MAX;
-#pragma unroll
-  for (int n = 0; n < NQ; n++) {
-    const int t = row0 + 32 * n;
-    const bool on = t < p.q_len;
-    span[n] = on ? row_span(p, b, t) : make_int2(0, 0);
-    if (on) {
-      in_lo = max(in_lo, span[n].x);
-      in_hi = min(in_hi, span[n].y);
-      if (span[n].x < span[n].y) {
-        lo = min(lo, span[n].x);
-        hi = max(hi, span[n].y);
-      }
-    }
+  frag<E> q[D / 16];
+  {
     const E *row = tok_row<E>(p.q, b, on ? t : 0, head);
 #pragma unroll
     for (int k = 0; k < D / 16; k++) {
       const int chunk = 2 * k + (lane >> 5);
-      q[n][k] = row_operand<E>(row, chunk, on && 8 * chunk < p.dim);
+      q[k] = row_operand<E>(row, chunk, on && 8 * chunk < p.dim);
     }
   }
-  lo = __builtin_amdgcn_readfirstlane(wave_min(lo));
-  hi = __builtin_amdgcn_readfirstlane(wave_max(hi));
-  in_lo = __builtin_amdgcn_readfirstlane(wave_max(in_lo));
-  in_hi = __builtin_amdgcn_readfirstlane(wave_min(in_hi));
+  const bool some = span.x < span.y;
+  const int lo = __builtin_amdgcn_readfirstlane(wave_min(some ? span.x : INT32_MAX));
+  const int hi = __builtin_amdgcn_readfirstlane(wave_max(span.y));
+  const int in_lo = __builtin_amdgcn_readfirstlane(wave_max(on ? span.x : 0));
+  const int in_hi = __builtin_amdgcn_readfirstlane(wave_min(on ? span.y : INT32_MAX));
   if (lane == 0) range[wave] = make_int2(lo, hi);
   __syncthreads();
   int first = INT32_MAX, end = 0;
@@ -212,7 +210,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p
 
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
-  Softmax<E, D, NQ> sm;
+  Softmax<E, D> sm;
   sm.init();
   using Tile = Copy<E, D, 256, KT>;
   if (first < end) {
@@ -234,44 +232,38 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attn_fwd(AttnK p
     turn(j, b0, b1);
     if (j + 1 < end) turn(j + 1, b1, b0);
   }
+  sm.l = other_half(sm.l, false);
 
+  const float l = sm.l, inv = l == 0.0f ? 0.0f : 1.0f / l;
+  bool nan = false;
 #pragma unroll
-  for (int n = 0; n < NQ; n++) {
-    const int t = row0 + 32 * n;
-    const bool on = t < p.q_len;
-    const float l = other_half(sm.l[n], false), inv = l == 0.0f ? 0.0f : 1.0f / l;
-    bool nan = false;
+  for (int d = 0; d < D / 32; d++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      sm.o[d][i] *= inv;
+      nan |= sm.o[d][i] != sm.o[d][i];
+    }
+  uint64_t again = __builtin_amdgcn_ballot_w64(on && nan);
+  again = (again | again >> 32) & 0xffffffffu;
+  if (on && !(again >> (lane & 31) & 1)) {
+    E *o = tok_row<E>(p.o, b, t, head);
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        sm.o[n][d][i] *= inv;
-        nan |= sm.o[n][d][i] != sm.o[n][d][i];
+      for (int i = 0; i < 16; i += 4) {
+        const int e = 32 * d + acc_row(i, lane);
+        const f32x16 x = sm.o[d];
+        if (e < p.dim) store4(o + e, (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]});
       }
-    uint64_t again = __builtin_amdgcn_ballot_w64(on && nan);
-    again = (again | again >> 32) & 0xffffffffu;
-    const bool keep = on && !(again >> (lane & 31) & 1);
-    if (keep) {
-      E *o = tok_row<E>(p.o, b, t, head);
-#pragma unroll
-      for (int d = 0; d < D / 32; d++)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int e = 32 * d + acc_row(i, lane);
-          const f32x16 x = sm.o[n][d];
-          if (e < p.dim) store4(o + e, (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]});
-        }
-      if (lane < 32)
-        p.lse[((int64_t)b * p.q_heads + head) * p.q_len + t] =
-            l == 0.0f ? -INFINITY
-                      : ((sm.m[n] == -INFINITY ? 0.0f : sm.m[n]) + __builtin_amdgcn_logf(l)) *
-                            ATTN_LN2;
-    }
-    while (again) {
-      const int r = __builtin_ctzll(again);
-      again &= again - 1;
-      redo_row<E>(p, b, head, tile * 128 * NQ + wave * 32 * NQ + 32 * n + r, lane);
-    }
+    if (lane < 32)
+      p.lse[((int64_t)b * p.q_heads + head) * p.q_len + t] =
+          l == 0.0f ? -INFINITY
+                    : ((sm.m == -INFINITY ? 0.0f : sm.m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
+  }
+  while (again) {
+    const int r = __builtin_ctzll(again);
+    again &= again - 1;
+    redo_row<E>(p, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
@@ -300,25 +292,25 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   const bool on = r < rows;
   const int t = on ? (int)(r / p.share) : 0, head = kvh * p.share + (on ? (int)(r % p.share) : 0);
 
-  frag<E> q[1][D / 16];
+  frag<E> q[D / 16];
   const E *row = tok_row<E>(p.q, b, t, head);
 #pragma unroll
   for (int k = 0; k < D / 16; k++) {
     const int chunk = 2 * k + (lane >> 5);
-    q[0][k] = row_operand<E>(row, chunk, on && 8 * chunk < p.dim);
+    q[k] = row_operand<E>(row, chunk, on && 8 * chunk < p.dim);
   }
-  int2 span[1] = {on ? row_span(p, b, t) : make_int2(0, 0)};
+  int2 span = on ? row_span(p, b, t) : make_int2(0, 0);
   const int p0 = part * p.split_keys, p1 = min(p0 + p.split_keys, p.kv_len);
-  const int lo = max(wave_min(span[0].x < span[0].y ? span[0].x : INT32_MAX), p0);
-  const int hi = min(wave_max(span[0].y), p1);
-  const int in_lo = wave_max(on ? span[0].x : 0), in_hi = wave_min(on ? span[0].y : INT32_MAX);
-  span[0].x = max(span[0].x, p0);
-  span[0].y = min(span[0].y, p1);
-  if (span[0].x >= span[0].y) span[0] = make_int2(0, 0);
+  const int lo = max(wave_min(span.x < span.y ? span.x : INT32_MAX), p0);
+  const int hi = min(wave_max(span.y), p1);
+  const int in_lo = wave_max(on ? span.x : 0), in_hi = wave_min(on ? span.y : INT32_MAX);
+  span.x = max(span.x, p0);
+  span.y = min(span.y, p1);
+  if (span.x >= span.y) span = make_int2(0, 0);
 
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
-  Softmax<E, D, 1> sm;
+  Softmax<E, D> sm;
   sm.init();
   using Tile = Copy<E, D, 64, FT>;
   const int first = __builtin_amdgcn_readfirstlane(lo < hi ? lo / FT + wave : 0);
@@ -347,10 +339,10 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   }
 
   // Join the waves: a common reference, then sums in LDS in wave order.
-  sm.l[0] = other_half(sm.l[0], false);
+  sm.l = other_half(sm.l, false);
   if (lane < 32) {
-    ml[wave][0][lane] = sm.m[0];
-    ml[wave][1][lane] = sm.l[0];
+    ml[wave][0][lane] = sm.m;
+    ml[wave][1][lane] = sm.l;
   }
   __syncthreads();
   float m = -INFINITY, l = 0.0f;
@@ -359,8 +351,11 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
   for (int w = 0; w < 4; w++)
-    l += ml[w][1][lane & 31] * __builtin_amdgcn_exp2f(ml[w][0][lane & 31] - ref);
-  const float mine = __builtin_amdgcn_exp2f(sm.m[0] - ref);
+    l += ml[w][1][lane & 31] *
+         (ml[w][0][lane & 31] == -INFINITY ? 1.0f
+                                           : __builtin_amdgcn_exp2f(ml[w][0][lane & 31] - ref));
+  // (a wave without keys has zeros, one with NaN scores alone NaN: both as they are)
+  const float mine = sm.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm.m - ref);
   float *sum = (float *)&b0[0][0][0];  // [32][D + 4]
   for (int w = 0; w < 4; w++) {
     if (w == wave) {
@@ -369,7 +364,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
       for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const f32x16 o = sm.o[0][d];
+          const f32x16 o = sm.o[d];
           f32x4 x = {o[i], o[i + 1], o[i + 2], o[i + 3]};
           f32x4 *at4 = (f32x4 *)(to + 32 * d + acc_row(i, lane));
           x *= mine;
@@ -424,40 +419,61 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
 }
 
 // Joins the parts of one row: a block a row, 32 lanes with four elements each for
-// every eighth part.
+// every eighth part, in one pass (what bounds it is latency: the loads of four parts
+// are under way together, and nothing is read first to start them).
 template <class E>
 __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
-  __shared__ float tops[4];
   __shared__ __attribute__((aligned(16))) float sums[8][132];
   const int tid = threadIdx.x, lane = tid & 63, e = 4 * (tid & 31);
   const int64_t all = (int64_t)p.batch * p.q_heads * p.q_len, row = blockIdx.x;
-  float top = -INFINITY;
-  for (int s = tid; s < p.splits; s += 256) top = fmaxf(top, p.part_ml[2 * (s * all + row)]);
-  top = wave_fmax(top);
-  if (lane == 0) tops[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float l = 0.0f;
+  float m = -INFINITY, l = 0.0f;
   f32x4 o = 0.0f;
-#pragma unroll 4
-  for (int s = tid >> 5; s < p.splits; s += 8) {
-    const int64_t slot = s * all + row;
-    const float w = __builtin_amdgcn_exp2f(p.part_ml[2 * slot] - ref);
-    l = fmaf(p.part_ml[2 * slot + 1], w, l);
-    if (e < p.dim) o += *(const f32x4 *)(p.part_o + slot * p.dim + e) * w;
+  for (int s0 = tid >> 5; s0 < p.splits; s0 += 32) {
+    float2 ml[4];
+    f32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const bool in = s0 + 8 * i < p.splits;
+      const int64_t slot = (in ? s0 + 8 * i : 0) * all + row;
+      ml[i] = *(const float2 *)(p.part_ml + 2 * slot);
+      x[i] = *(const f32x4 *)(p.part_o + slot * p.dim + (e < p.dim ? e : 0));
+      if (!in) ml[i].x = -INFINITY;
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 4; i++) top = fmaxf(top, ml[i].x);
+    const float shrink = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    l *= shrink;
+    o *= shrink;
+    m = top;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (s0 + 8 * i >= p.splits) continue;
+      // a part without keys holds zeros, one of NaN scores alone NaN: both as they are
+      const float w = ml[i].x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - top);
+      l = fmaf(ml[i].y, w, l);
+      o += x[i] * w;
+    }
   }
   *(f32x4 *)&sums[tid >> 5][e] = o;
-  if ((tid & 31) == 0) sums[tid >> 5][128] = l;
+  if ((tid & 31) == 0) {
+    sums[tid >> 5][128] = l;
+    sums[tid >> 5][129] = m;
+  }
   __syncthreads();
   if (tid >= 64) return;
+  float ref = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; i++) ref = fmaxf(ref, sums[i][129]);
+  ref = ref == -INFINITY ? 0.0f : ref;
   l = 0.0f;
   float o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    l += sums[i][128];
-    o0 += sums[i][lane];
-    o1 += sums[i][lane + 64];
+    const float w = sums[i][129] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sums[i][129] - ref);
+    l = fmaf(sums[i][128], w, l);
+    o0 = fmaf(sums[i][lane], w, o0);
+    o1 = fmaf(sums[i][lane + 64], w, o1);
   }
   const int64_t bh = row / p.q_len;
   const int t = (int)(row - bh * p.q_len), b = (int)(bh / p.q_heads);
@@ -486,7 +502,9 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
     return hipGetLastError();
   }
   const int tiles = (p.q_len + 127) / 128;
-  k_attn_fwd<E, D, 1><<<p.batch * p.q_heads * tiles, 256, 0, st>>>(p, tiles);
+  const int blocks = p.batch * p.q_heads * tiles * p.passes;
+  if (D == 128 && p.dim <= 96) k_attn_fwd<E, 96><<<blocks, 256, 0, st>>>(p, tiles);
+  else k_attn_fwd<E, D><<<blocks, 256, 0, st>>>(p, tiles);
   return hipGetLastError();
 }
 
@@ -494,7 +512,9 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
 
 // The split of the keys that a call takes, 0: the form for many rows.
 //   few rows: no more than 32 rows read a key head (one block of rows), or the
-//   form for many rows would leave most of 256 compute units without work.
+//   form for many rows would have fewer blocks than 256 compute units.
+// Measured, few and many: 2331 tokens, 8 heads of 64 (152 blocks) 23 and 30 us; 6037
+// tokens in four sequences, 12 heads of 80 on 4 (576 blocks) 195 and 58.
 void gs_attn_plan(AttnK *p) {
   const int64_t rows = (int64_t)p->q_len * p->share, row_tiles = (rows + 31) / 32;
   const int64_t many = (int64_t)p->batch * p->q_heads * ((p->q_len + 127) / 128);
@@ -502,8 +522,10 @@ void gs_attn_plan(AttnK *p) {
   p->split_keys = 0;
   if (!p->batch || !p->q_len || (rows > 32 && many >= 256)) return;
   const int64_t blocks = (int64_t)p->batch * p->kv_heads * row_tiles;
-  // about 512 workgroups, none with fewer than 256 keys
-  int64_t splits = (512 + blocks - 1) / blocks;
+  // one round of workgroups (by their LDS, one on each of 256 compute units for heads
+  // above 64, else two), none with fewer than 256 keys
+  const int64_t room = p->dim <= 64 ? 512 : 256;
+  int64_t splits = blocks < room ? room / blocks : 1;
   const int64_t most = (p->kv_len + 255) / 256;
   splits = splits < most ? splits : most;
   if (splits < 1) splits = 1;
@@ -512,7 +534,16 @@ void gs_attn_plan(AttnK *p) {
   p->splits = (int)(p->kv_len ? (p->kv_len + p->split_keys - 1) / p->split_keys : 1);
 }
 
-hipError_t gs_launch_attn_fwd(const AttnK &p, int dtype, hipStream_t st) {
+// Whether blocks of 128 rows are launched twice: with spans, unless there are so many
+// of them that one with two sequences' keys is hidden among the others. Measured, 6037
+// tokens in four sequences, 12 heads of 80 (576 blocks): 78 us with one pass, 58 with
+// two; where no block has rows of two, 56 and 57.
+int gs_attn_passes(const AttnK &p) {
+  return p.spans && (int64_t)p.batch * p.q_heads * ((p.q_len + 127) / 128) < 4096 ? 2 : 1;
+}
+
+hipError_t gs_launch_attn_fwd(AttnK p, int dtype, hipStream_t st) {
+  p.passes = gs_attn_passes(p);
   if (dtype == GS_BF16) return p.dim <= 64 ? launch<bf16_t, 64>(p, st) : launch<bf16_t, 128>(p, st);
   return p.dim <= 64 ? launch<f16_t, 64>(p, st) : launch<f16_t, 128>(p, st);
 }

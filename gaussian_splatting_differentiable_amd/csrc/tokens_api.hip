@@ -10,8 +10,8 @@ hipError_t gs_launch_qk_bwd(const QkK &p, int dtype, hipStream_t st);
 int gs_qk_bwd_blocks(int64_t batch, int64_t tokens, int q_heads, int k_heads, int lanes);
 void gs_attn_plan(AttnK *p);
 void gs_attn_bwd_plan(AttnK *p, bool masked);
-hipError_t gs_launch_attn_fwd(const AttnK &p, int dtype, hipStream_t st);
-hipError_t gs_launch_attn_bwd(const AttnK &p, int dtype, hipStream_t st);
+hipError_t gs_launch_attn_fwd(AttnK p, int dtype, hipStream_t st);
+hipError_t gs_launch_attn_bwd(AttnK p, int dtype, hipStream_t st);
 
 namespace {
 

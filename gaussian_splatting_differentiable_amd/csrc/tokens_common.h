@@ -88,6 +88,7 @@ struct AttnK {
   int64_t span_stride;
   TokK q, k, v, o;
   float *lse;
+  int passes;  // 2: blocks of rows are launched twice (attention_common.h: apart)
   // the split form
   int splits, split_keys;
   float *part_o, *part_ml;

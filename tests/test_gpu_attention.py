@@ -222,6 +222,21 @@ def test_splits_agree_with_one_pass():
     ref.check("lse", full_lse[:, :, :2], want["lse"])
 
 
+def test_nan_in_a_row_shows_in_parts_too():
+    """A NaN query, a NaN key and a NaN value in a long cache that is computed in parts."""
+    tok = _tokens()
+    q, k, v, _ = _inputs(31, 1, 3, 9000, 2, 2, 64, BF)
+    q[:, 1] = math.nan
+    v[:, 5000, 1, 7] = math.nan
+    o, lse = tok.attention(q, k, v)
+    assert torch.isnan(o[:, 1]).all() and torch.isnan(lse[:, :, 1]).all()
+    assert torch.isfinite(o[:, 0, 0]).all() and torch.isfinite(lse[:, :, 0]).all()
+    assert torch.isnan(o[:, 0, 1, 7]) and int(torch.isnan(o[:, 0, 1]).sum()) == 1
+    k[:, 8999, 0, 3] = math.nan
+    o, lse = tok.attention(q, k, v)
+    assert torch.isnan(o[:, 0, 0]).all() and torch.isnan(lse[:, 0]).all()
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes (2^31 elements); the queries see its end."""
     n, d = 2_200_000, 128
