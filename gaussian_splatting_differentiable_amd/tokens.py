@@ -99,7 +99,7 @@ def _base(name, shape, dtype, device):
 
 def _elsewhere(stream, device):
     """Whether a call is not for the current stream of the current device."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != torch._C._cuda_getDevice()
 
 
 @contextlib.contextmanager
@@ -139,7 +139,7 @@ def _list2d(name, t, batch, n, tail, device):
 
 def _out(name, out, like):
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     _same(name, out, like.shape, like.dtype, like.device)
     return out
 
@@ -233,16 +233,16 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_
     dq = dk = gq = gk = oq = ok = dwq = dwk = ws = None
     if q is not None:
         _same("dq_out", dq_out, q.shape, q.dtype, dev)
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        dq = _out("dq", None, q)
         gq, oq = _tokens(dq_out), _tokens(dq)
     if k is not None:
         _same("dk_out", dk_out, k.shape, k.dtype, dev)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        dk = _out("dk", None, k)
         gk, ok = _tokens(dk_out), _tokens(dk)
     if q_weight is not None:
-        dwq = torch.empty(q_weight.shape, dtype=torch.float32, device=dev)
+        dwq = _out("dq_weight", None, q_weight)
     if k_weight is not None:
-        dwk = torch.empty(k_weight.shape, dtype=torch.float32, device=dev)
+        dwk = _out("dk_weight", None, k_weight)
     L = _lib()
     if dwq is not None or dwk is not None:
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
@@ -331,9 +331,9 @@ def attention_bwd(do, q, k, v, o, lse, *, spans=None, causal=False, scale=None, 
         with _there(stream, dev, (do, q, k, v, o, lse, spans, workspace)):
             return attention_bwd(do, q, k, v, o, lse, spans=spans, causal=causal, scale=scale,
                                  workspace=workspace)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dq = _out("dq", None, q)
+    dk = _out("dk", None, k)
+    dv = _out("dv", None, v)
     ws = _workspace(size, workspace, dev)
     _check(_lib().gs_attention_bwd(shape, _tokens(do), _tokens(q), _tokens(k), _tokens(v), at,
                                    _tokens(o), sums, _tokens(dq), _tokens(dk), _tokens(dv),
