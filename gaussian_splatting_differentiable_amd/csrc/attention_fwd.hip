@@ -4,9 +4,13 @@
 //
 // One pass over the keys with a running reference m_i and sum l_i (32 bits, in
 // powers of two): p = 2^(s - m), o and l scaled by 2^(m - m') when the reference
-// moves. It moves only when some score of the wave passes it by 8 (p <= 256
-// stays exact enough in 16 bits: rounding is relative), so most tiles skip the
-// 16 D / 32 multiplications per row block.
+// moves. It moves only when some score of the wave passes it by 8 (rounding is
+// relative, so p above 1 are as exact as those below).
+// With many rows a wave looks for its largest scores in the first tile only. Later
+// tiles compute p with the reference that is there; if a lane's sum of them passes 2^13
+// (or is NaN), the wave computes the tile's scores again and looks. Measured, 2 x 8192
+// tokens, 16 heads of 64: 690 us, looking at every tile 714; with few rows (2331 tokens,
+// 8 heads of 64) 27 us and 24, there every tile is looked at.
 // p is rounded to the inputs' 16-bit type for the second product, as matrix
 // instructions take it; l sums the unrounded p.
 #include "attention_common.h"
@@ -51,14 +55,19 @@ __device__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
         l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
 }
 
+// Largest sum of a lane's p of a tile that needs no look: each of them fits fp16.
+constexpr float P_ROOM = 8192.0f;
+
 // A wave's running softmax over its 32 rows and its share of o.
 template <class E, int D>
 struct Softmax {
   f32x16 o[D / 32];
   float m, l;
 
-  __device__ __forceinline__ void init() {
-    m = -INFINITY;
+  // sees: whether the lane's row sees any key (one that does not has no reference to
+  // wait for).
+  __device__ __forceinline__ void init(bool sees) {
+    m = sees ? -INFINITY : 0.0f;
     l = 0.0f;
 #pragma unroll
     for (int d = 0; d < D / 32; d++) o[d] = 0.0f;
@@ -74,63 +83,71 @@ struct Softmax {
     // of 96, else 256; that one also reads no values early).
     constexpr int STEPS = D / 16, AHEAD = D == 96 ? 2 : 4;
     f32x16 s[NS];
-    frag<E> a[NS][STEPS];
-    auto read = [&](int k) {
+    frag<E> v0[2][D / 32];
+    float sum;
+    bool look = NS == 1 || __builtin_amdgcn_ballot_w64(m == -INFINITY);
+    for (;;) {
+      frag<E> a[NS][STEPS];
+      auto read = [&](int k) {
 #pragma unroll
-      for (int b = 0; b < NS; b++) a[b][k] = lds_rows<E, D>(kt, 32 * b, k, lane);
-    };
+        for (int b = 0; b < NS; b++) a[b][k] = lds_rows<E, D>(kt, 32 * b, k, lane);
+      };
 #pragma unroll
-    for (int k = 0; k < AHEAD; k++) read(k);
+      for (int k = 0; k < AHEAD; k++) read(k);
 #pragma unroll
-    for (int k = 0; k < STEPS; k++) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (k + AHEAD < STEPS) read(k + AHEAD);
+      for (int k = 0; k < STEPS; k++) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (k + AHEAD < STEPS) read(k + AHEAD);
 #pragma unroll
-      for (int b = 0; b < NS; b++) {
-        if (k == 0) s[b] = 0.0f;
-        s[b] = mfma(a[b][k], q[k], s[b]);
+        for (int b = 0; b < NS; b++) {
+          if (k == 0) s[b] = 0.0f;
+          s[b] = mfma(a[b][k], q[k], s[b]);
+        }
       }
-    }
-    if (!full) {
+      if (!full) {
+#pragma unroll
+        for (int b = 0; b < NS; b++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int j = key0 + 32 * b + acc_row(i, lane);
+            if ((unsigned)(j - span.x) >= (unsigned)(span.y - span.x)) s[b][i] = -INFINITY;
+          }
+      }
+      // the first 32 keys' values, on their way while the softmax is computed
+#pragma unroll
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+          if (D != 96) v0[k][d] = lds_cols<E, D>(vt, 16 * k, d, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      if (look) {
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < NS; b++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][i]);
+        top = other_half(top, true) * scale_log2;
+        if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+          const float to = fmaxf(m, top), ref = to == -INFINITY ? 0.0f : to;
+          const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
+          m = to;
+          l *= shrink;
+#pragma unroll
+          for (int d = 0; d < D / 32; d++) o[d] *= shrink;
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      sum = 0.0f;
 #pragma unroll
       for (int b = 0; b < NS; b++)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-          const int j = key0 + 32 * b + acc_row(i, lane);
-          if ((unsigned)(j - span.x) >= (unsigned)(span.y - span.x)) s[b][i] = -INFINITY;
+          s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], scale_log2, -ref));
+          sum += s[b][i];
         }
+      if (look || !__builtin_amdgcn_ballot_w64(!(sum <= P_ROOM))) break;
+      look = true;
     }
-    // the first 32 keys' values, on their way while the softmax is computed
-    frag<E> v0[2][D / 32];
-#pragma unroll
-    for (int k = 0; k < 2; k++)
-#pragma unroll
-      for (int d = 0; d < D / 32; d++)
-        if (D != 96) v0[k][d] = lds_cols<E, D>(vt, 16 * k, d, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    float top = s[0][0];
-#pragma unroll
-    for (int b = 0; b < NS; b++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][i]);
-    top = other_half(top, true) * scale_log2;
-    if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
-      const float to = fmaxf(m, top), ref = to == -INFINITY ? 0.0f : to;
-      const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
-      m = to;
-      l *= shrink;
-#pragma unroll
-      for (int d = 0; d < D / 32; d++) o[d] *= shrink;
-    }
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int b = 0; b < NS; b++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) {
-        s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], scale_log2, -ref));
-        sum += s[b][i];
-      }
     l += sum;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -160,7 +177,7 @@ struct Softmax {
 // to 96 have a form of 96, of which three blocks fit a compute unit: 6037 tokens in four
 // sequences, 12 heads of 80: 58 us, in the form of 128 73; 2 x 2048 tokens, 12 heads of
 // 80: 61 and 70. 64 rows a wave instead of 32 were slower: 2 x 8192 tokens, 16 heads of
-// 64: 808 us, with 32 690 (the exponentials of heads of 64 take as long as the products).
+// 64: 808 us, with 32 714 (the exponentials of heads of 64 take as long as the products).
 template <class E, int D>
 __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
@@ -211,7 +228,7 @@ __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int 
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
   Softmax<E, D> sm;
-  sm.init();
+  sm.init(span.x < span.y);
   using Tile = Copy<E, D, 256, KT>;
   if (first < end) {
     Tile::issue(ks, first * KT, b0[0], tid);
@@ -311,7 +328,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   const Stream<E> ks = {tok_row<E>(p.k, b, 0, kvh), p.k.ts, p.kv_len, p.dim};
   const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
   Softmax<E, D> sm;
-  sm.init();
+  sm.init(span.x < span.y);
   using Tile = Copy<E, D, 64, FT>;
   const int first = __builtin_amdgcn_readfirstlane(lo < hi ? lo / FT + wave : 0);
   const int end = __builtin_amdgcn_readfirstlane(lo < hi ? (hi + FT - 1) / FT : 0);
@@ -340,6 +357,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
 
   // Join the waves: a common reference, then sums in LDS in wave order.
   sm.l = other_half(sm.l, false);
+  if (sm.l == 0.0f) sm.m = -INFINITY;  // a row that sees nothing here has no reference
   if (lane < 32) {
     ml[wave][0][lane] = sm.m;
     ml[wave][1][lane] = sm.l;

@@ -166,6 +166,22 @@ def test_scores_far_apart_and_reference_moves():
                  do.repeat(1, 1, 32, 1))
 
 
+@pytest.mark.parametrize("H,n", [(64, 700), (2, 700)])
+@pytest.mark.parametrize("rise", [0.5, 8.0, 12.0, 40.0])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_scores_that_rise_along_the_keys(H, n, rise, dtype):
+    """Each 64 keys' scores pass those before by `rise` powers of two, for every second query;
+    the others' fall as fast. The gradients where p spans less than its 32 bits can (2^-126),
+    or than its 16 bits beside the largest in fp16; the bounds leave underflow out."""
+    q, k, v, do = _inputs(21, 1, n, n, H, H, 64, dtype)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    q[:, ::2, :, 0] = -1.0
+    step = rise * math.log(2.0) / 64
+    k[0, :, :, 0] = (torch.arange(n, device="cuda") * step - n * step / 2)[:, None].to(dtype)
+    span = 120 if dtype == BF else 24
+    _compare(q, k, v, do if rise * n / 64 < span else None, scale=1.0)
+
+
 def test_long_row_of_small_probabilities_in_fp16():
     """Probabilities below fp16's normal range (2^-14) keep their precision in the gradient."""
     q, k, v, do = _inputs(13, 1, 33, 20000, 1, 1, 64, FP)
