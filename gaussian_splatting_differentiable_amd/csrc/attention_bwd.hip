@@ -326,10 +326,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
   __shared__ float tops[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = wave >> 2;
-  const int item = die_order(blockIdx.x, gridDim.x);
-  const int piece = item % p.kv_parts, whole = item / p.kv_parts;
-  const int bh = whole / tiles, b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
-  const int key0 = (whole - bh * tiles) * 128, mine0 = key0 + 32 * (wave & 3);
+  const bool uneven = p.causal || p.spans;
+  const Item it = die_item(blockIdx.x, p.batch * p.kv_heads, tiles, p.kv_parts, uneven);
+  if (it.head < 0) return;
+  const int piece = it.part, bh = it.head, b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
+  // (causal: the first keys are seen by the most queries)
+  const int key0 = (uneven ? tiles - 1 - it.tile : it.tile) * 128, mine0 = key0 + 32 * (wave & 3);
   const int key = mine0 + (lane & 31);
   const bool on = key < p.kv_len;
 
@@ -589,10 +591,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
   __shared__ float tops[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int once = gridDim.x / p.passes, pass = blockIdx.x / once;
-  const int run = die_order(blockIdx.x % once, once);
-  const int piece = run % p.q_parts, whole = run / p.q_parts;
-  const int2 bt = block_item(p, whole, p.batch * p.q_heads, tiles);
-  const int bh = bt.x, tile0 = bt.y * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
+  const Item it = die_item(blockIdx.x % once, p.batch * p.q_heads, tiles, p.q_parts,
+                           p.causal || p.spans);
+  if (it.head < 0) return;
+  const int piece = it.part;
+  const int bh = it.head, tile0 = it.tile * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
   const int kvh = head / p.share, t = tile0 + wave * 32 + (lane & 31);
   bool on = t < p.q_len;
   int2 span = on ? row_span(p, b, t) : make_int2(0, 0);
@@ -779,13 +782,13 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
   if (err != hipSuccess) return err;
   const int k_tiles = (p.kv_len + 127) / 128, tiles = (p.q_len + 127) / 128;
   if (k_tiles) {
-    k_attn_bwd_kv<E, D><<<p.batch * p.kv_heads * k_tiles * p.kv_parts, 512, 0, st>>>(p, k_tiles,
-                                                                                    q_tiles);
+    k_attn_bwd_kv<E, D><<<die_blocks(p.batch * p.kv_heads, k_tiles, p.kv_parts), 512, 0, st>>>(
+        p, k_tiles, q_tiles);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   if (tiles) {
-    const int blocks = p.batch * p.q_heads * tiles * p.q_parts * p.passes;
+    const int blocks = die_blocks(p.batch * p.q_heads, tiles, p.q_parts) * p.passes;
     if (D == 128 && p.dim <= 96) k_attn_bwd_q<E, 96><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
     else k_attn_bwd_q<E, D><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
     err = hipGetLastError();

@@ -97,14 +97,37 @@ __device__ __forceinline__ int die_order(int block, int blocks) {
   return die * per + min(die, rest) + (block >> 3);
 }
 
-// Head (x) and row tile (y) of an item: a head's tiles in a row, so that they share
-// its keys in their die's L2. Causal rows see more keys the later they are: there
-// the last tiles of a die's heads come first, so that the longest blocks do.
-__device__ __forceinline__ int2 block_item(const AttnK &p, int item, int heads, int tiles) {
-  if (!p.causal) return make_int2(item / tiles, item % tiles);
-  const int per = max(heads >> 3, 1), group = item / (per * tiles);
-  const int rest = item - group * per * tiles, n = min(per, heads - group * per);
-  return make_int2(group * per + rest % n, tiles - 1 - rest / n);
+// The dies that share a group of heads: one for each group where the heads divide
+// evenly, else 2, 4 or 8 that take its items in turn.
+inline __host__ __device__ int group_dies(int heads) { return 8 / min(heads & -heads, 8); }
+
+// Workgroups for `parts` of every row tile of every head, a multiple of 8.
+inline int die_blocks(int heads, int tiles, int parts) {
+  const int dies = group_dies(heads);
+  return 8 * (((heads * dies >> 3) * tiles * parts + dies - 1) / dies);
+}
+
+struct Item {
+  int head, tile, part;  // head < 0: none (the last ones of a group)
+};
+
+// What workgroup `block` works on. Its die's heads share their streamed rows in the
+// die's L2: a head's tiles follow each other. Where a mask makes rows' keys uneven,
+// the heads do, from the last tile (causal rows see more keys the later they are) to
+// the first: long blocks come early, and those that a compute unit takes differ.
+__device__ __forceinline__ Item die_item(int block, int heads, int tiles, int parts, bool uneven) {
+  const int dies = group_dies(heads), n = heads * dies >> 3, die = block & 7;
+  const int at = (block >> 3) * dies + die % dies, whole = at / parts;
+  Item x = {-1, 0, at - whole * parts};
+  if (whole >= n * tiles) return x;
+  if (uneven) {
+    x.tile = tiles - 1 - whole / n;
+    x.head = die / dies * n + whole % n;
+  } else {
+    x.tile = whole % tiles;
+    x.head = die / dies * n + whole / tiles;
+  }
+  return x;
 }
 
 // ---- tiles in LDS: KT rows of D elements in 16-byte chunks. Chunk c of row r is

@@ -187,9 +187,9 @@ __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int 
   __shared__ int2 range[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int once = gridDim.x / p.passes, pass = blockIdx.x / once;
-  const int item = die_order(blockIdx.x % once, once);
-  const int2 bt = block_item(p, item, p.batch * p.q_heads, tiles);
-  const int bh = bt.x, tile0 = bt.y * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
+  const Item it = die_item(blockIdx.x % once, p.batch * p.q_heads, tiles, 1, p.causal || p.spans);
+  if (it.head < 0) return;
+  const int bh = it.head, tile0 = it.tile * 128, b = bh / p.q_heads, head = bh - b * p.q_heads;
   const int kvh = head / p.share, t = tile0 + wave * 32 + (lane & 31);
   bool on = t < p.q_len;
   int2 span = on ? row_span(p, b, t) : make_int2(0, 0);
@@ -520,7 +520,7 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
     return hipGetLastError();
   }
   const int tiles = (p.q_len + 127) / 128;
-  const int blocks = p.batch * p.q_heads * tiles * p.passes;
+  const int blocks = die_blocks(p.batch * p.q_heads, tiles, 1) * p.passes;
   if (D == 128 && p.dim <= 96) k_attn_fwd<E, 96><<<blocks, 256, 0, st>>>(p, tiles);
   else k_attn_fwd<E, D><<<blocks, 256, 0, st>>>(p, tiles);
   return hipGetLastError();
@@ -529,24 +529,31 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
 }  // namespace
 
 // The split of the keys that a call takes, 0: the form for many rows.
-//   few rows: no more than 32 rows read a key head (one block of rows), or the
-//   form for many rows would have fewer blocks than 256 compute units.
-// Measured, few and many: 2331 tokens, 8 heads of 64 (152 blocks) 23 and 30 us; 6037
-// tokens in four sequences, 12 heads of 80 on 4 (576 blocks) 195 and 58.
+//   few rows: no more than 32 rows read a key head (one block of rows), or the blocks
+//   of 32 rows are no more than run at once (by their LDS, one on each of 256 compute
+//   units for heads above 64, else two), or twice that where a mask makes them uneven.
+// Measured, few and many, 8 heads: 2048 tokens, heads of 64 (512 blocks) 24 and 34 us,
+// 3000 tokens (752) 51 and 48, 3000 causal 37 and 46; 1024 tokens, heads of 128 (256) 17
+// and 26, 1536 (384) 38 and 36, 2048 causal (512) 38 and 44, 3000 causal (752) 66 and 61.
 void gs_attn_plan(AttnK *p) {
   const int64_t rows = (int64_t)p->q_len * p->share, row_tiles = (rows + 31) / 32;
-  const int64_t many = (int64_t)p->batch * p->q_heads * ((p->q_len + 127) / 128);
+  const int64_t blocks = (int64_t)p->batch * p->kv_heads * row_tiles;
+  const int64_t room = p->dim <= 64 ? 512 : 256;
   p->splits = 0;
   p->split_keys = 0;
-  if (!p->batch || !p->q_len || (rows > 32 && many >= 256)) return;
-  const int64_t blocks = (int64_t)p->batch * p->kv_heads * row_tiles;
-  // one round of workgroups (by their LDS, one on each of 256 compute units for heads
-  // above 64, else two), none with fewer than 256 keys
-  const int64_t room = p->dim <= 64 ? 512 : 256;
+  if (!blocks || (rows > 32 && blocks > (p->causal || p->spans ? 2 : 1) * room)) return;
+  // Parts: one round of workgroups, none with fewer than 256 keys, and where they cost
+  // less than they save. Joining them takes as long as a workgroup's 600 keys, and a
+  // row's part as long as 1/16 key (about 5.5 ns a key with heads of 64, 7.6 with 128).
+  // Measured, 8 heads of 64: 1 token, 512 keys 8.3 us whole and 9.3 in two parts, 1024
+  // keys 11.1 whole and 9.4 in four, 2048 keys 9.6 in eight; 64 tokens, 1024 keys 11.2
+  // and 9.8 in four; 512 tokens, 1024 keys 11.6 and 15.2 in four.
+  const int64_t all = (int64_t)p->batch * p->q_heads * p->q_len;
   int64_t splits = blocks < room ? room / blocks : 1;
-  const int64_t most = (p->kv_len + 255) / 256;
+  const int64_t most = p->kv_len / 256, even = (int64_t)sqrt(16.0 * p->kv_len / all);
   splits = splits < most ? splits : most;
-  if (splits < 1) splits = 1;
+  splits = splits < even ? splits : even;
+  if (splits < 2 || p->kv_len / splits + 600 + all * splits / 16 >= p->kv_len) splits = 1;
   const int64_t keys = ((p->kv_len + splits - 1) / splits + FT - 1) / FT * FT;
   p->split_keys = (int)(keys ? keys : FT);
   p->splits = (int)(p->kv_len ? (p->kv_len + p->split_keys - 1) / p->split_keys : 1);

@@ -128,12 +128,13 @@ int32_t attn_shape(const gs_attn_shape *s, AttnK *p) {
   p->scale = s->scale;
   p->scale_log2 = (float)((double)s->scale * 1.4426950408889634);
   p->span_stride = s->spans_stride;
-  gs_attn_plan(p);
   return GS_OK;
 }
 
-// Workspace of the forward's split form: o, then m and l of every part and row.
+// Workspace of the forward's split form: o, then m and l of every part and row. (Spans
+// may choose between forms without one, not its size.)
 size_t attn_layout(AttnK *p, void *ws) {
+  gs_attn_plan(p);
   if (p->splits <= 1) return 0;
   const size_t slots = (size_t)p->splits * p->batch * p->q_heads * p->q_len;
   const size_t o = round256(slots * p->dim * 4);

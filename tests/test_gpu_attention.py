@@ -111,6 +111,41 @@ def test_packed_sequences_share_one_span_list(H):
     assert not got["dk"][:, 235:].any() and not got["dv"][:, 235:].any()
 
 
+@pytest.mark.parametrize("d,dtype", [(64, BF), (80, FP), (96, BF), (128, FP)])
+@pytest.mark.parametrize("mask", ["none", "causal", "spans", "packed"])
+def test_masks_with_many_workgroups(mask, d, dtype):
+    """More rows than the form for few takes with a mask, in numbers of heads that the dies
+    share differently."""
+    B, H, n = {"none": (2, 100, 200), "causal": (1, 170, 200), "spans": (2, 84, 210),
+               "packed": (1, 203, 190)}[mask]
+    spans = None
+    if mask == "spans":
+        spans = _random_spans(41, B, n, n - 9)
+    elif mask == "packed":
+        spans = torch.zeros(n, 2, dtype=torch.int32)
+        for a, b in ((0, 50), (50, 140), (140, n - 11)):
+            spans[a:b, 0], spans[a:b, 1] = a, b
+        spans = spans.cuda()
+    m = n - 9 if mask == "spans" else n
+    _compare(*_inputs(42, B, n, m, H, H, d, dtype), spans=spans, causal=mask == "causal")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_masked_places_with_many_workgroups(bad):
+    q, k, v, do = _inputs(43, 2, 200, 200, 90, 90, 64, BF)
+    spans = torch.zeros(200, 2, dtype=torch.int32)
+    spans[:97, 1] = 97
+    spans[97:190, 0], spans[97:190, 1] = 97, 190
+    for t in (q, k, v, do):
+        t[:, 190:] = bad
+    _compare(q, k, v, do, spans=spans.cuda())
+    q[:, 100] = math.nan  # of the second sequence, in the first one's tile of rows
+    tok = _tokens()
+    o, lse = tok.attention(q, k, v, spans=spans.cuda())
+    nan = torch.isnan(o).any(3).any(2)
+    assert torch.equal(nan, torch.arange(200, device="cuda").expand(2, 200) == 100)
+
+
 def test_rows_that_all_see_nothing():
     q, k, v, do = _inputs(9, 2, 70, 90, 2, 2, 64, BF)
     got = _compare(q, k, v, do, spans=torch.zeros(70, 2, dtype=torch.int32).cuda())
