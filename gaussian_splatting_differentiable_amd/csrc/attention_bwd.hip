@@ -804,18 +804,25 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
 }  // namespace
 
 // Parts of a block's streamed tiles: enough to have a workgroup for each of 256
-// compute units, at least two where masks make the blocks uneven and they are no
-// more than one for each, every part with four tiles or more. A part costs the
-// write and the read of its 32-bit sums.
-// Measured, q_len 2331, 8 heads of 64 (152 blocks): dK and dV in one part 55 us, in two
-// 38 and their sum 7, in four 49 and 8; dQ in one part 35, in two 24 and their sum 5;
-// causal, 2 x 4096 queries, 16 heads of 128 on 4 (256 blocks), dK and dV: in one part
-// 576, in two 328 and their sum 15.
+// compute units, every part with four tiles or more. With spans at least two where the
+// blocks are no more than one for each; with causal rows, whose blocks are the most
+// uneven, as many as make two for each, of six tiles or more. A part costs the write and
+// the read of its 32-bit sums.
+// Measured, q_len 2331, 8 heads of 64 with spans (152 blocks): dK and dV in one part 55
+// us, in two 38 and their sum 7, in four 49 and 8; dQ in one part 35, in two 24 and their
+// sum 5. Causal, whole backward, 4096 tokens, 16 heads of 128 on 4 (128 blocks of keys):
+// in two parts 368 us, in four 300, in six 323; 2 x 4096 (256): dK and dV in one part
+// 576, in two 330 and their sum 15.
 void gs_attn_bwd_plan(AttnK *p, bool masked) {
-  auto parts = [masked](int64_t blocks, int64_t tiles) {
-    int64_t n = blocks ? (256 + blocks - 1) / blocks : 1;
-    if (masked && blocks <= 256) n = n < 2 ? 2 : n;
-    n = n < tiles / 4 ? n : tiles / 4;
+  const bool causal = p->causal;
+  auto parts = [masked, causal](int64_t blocks, int64_t tiles) {
+    if (!blocks) return 1;
+    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    int64_t n = (256 + blocks - 1) / blocks;
+    if (masked && !causal && blocks <= 256) n = n < 2 ? 2 : n;
+    n = least(n, tiles / 4);
+    const int64_t more = causal ? least((512 + blocks / 2) / blocks, tiles / 6) : 0;
+    n = n < more ? more : n;
     return (int)(n < 1 ? 1 : n < 16 ? n : 16);
   };
   p->kv_parts = parts((int64_t)p->batch * p->kv_heads * ((p->kv_len + 127) / 128),
