@@ -64,8 +64,9 @@ __device__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
   if (lane + 64 < p.dim) o[lane + 64] = (E)(a1 * p.scale);
 }
 
+// which: 1 dK, 2 dV, 3 both.
 template <class E>
-__device__ void redo_key(const AttnK &p, int b, int kvh, int key, int lane) {
+__device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int lane) {
   const E *k = tok_row<E>(p.k, b, key, kvh), *v = tok_row<E>(p.v, b, key, kvh);
   float k0 = 0.0f, k1 = 0.0f, v0 = 0.0f, v1 = 0.0f;
   for (int head = kvh * p.share; head < (kvh + 1) * p.share; head++)
@@ -99,13 +100,13 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int lane) {
       }
     }
   E *dk = tok_row<E>(p.dk, b, key, kvh), *dv = tok_row<E>(p.dv, b, key, kvh);
-  if (lane < p.dim) {
-    dk[lane] = (E)(k0 * p.scale);
-    dv[lane] = (E)v0;
+  if (which & 1) {
+    if (lane < p.dim) dk[lane] = (E)(k0 * p.scale);
+    if (lane + 64 < p.dim) dk[lane + 64] = (E)(k1 * p.scale);
   }
-  if (lane + 64 < p.dim) {
-    dk[lane + 64] = (E)(k1 * p.scale);
-    dv[lane + 64] = (E)v1;
+  if (which & 2) {
+    if (lane < p.dim) dv[lane] = (E)v0;
+    if (lane + 64 < p.dim) dv[lane + 64] = (E)v1;
   }
 }
 
@@ -246,11 +247,11 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
   }
 }
 
-// Largest of n floats at x, `stride` apart, by a block of NT threads.
+// Largest of n floats at x, by a block of NT threads.
 template <int NT>
-__device__ __forceinline__ float block_top(const float *x, int64_t n, int stride, float *lds) {
+__device__ __forceinline__ float block_top(const float *x, int n, float *lds) {
   float m = 0.0f;
-  for (int64_t i = threadIdx.x; i < n; i += NT) m = fmaxf(m, x[i * stride]);
+  for (int i = threadIdx.x; i < n; i += NT) m = fmaxf(m, x[i]);
   m = wave_fmax(m);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
@@ -265,14 +266,14 @@ __device__ __forceinline__ float block_top(const float *x, int64_t n, int stride
 // returns the rows (bits 0..31) that hold a NaN and were not stored.
 template <class E, int D>
 __device__ __forceinline__ uint32_t store_rows(const f32x16 (&acc)[D / 32], float by, E *row,
-                                               bool on, int dim, int lane, uint32_t skip) {
+                                               bool on, int dim, int lane) {
   bool nan = false;
 #pragma unroll
   for (int d = 0; d < D / 32; d++)
 #pragma unroll
     for (int i = 0; i < 16; i++) nan |= acc[d][i] != acc[d][i];
   const uint64_t bits = __builtin_amdgcn_ballot_w64(on && nan);
-  skip |= (uint32_t)bits | (uint32_t)(bits >> 32);
+  const uint32_t skip = (uint32_t)bits | (uint32_t)(bits >> 32);
   if (on && !(skip >> (lane & 31) & 1)) {
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
@@ -318,12 +319,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
   // sees that reads of one do not wait for copies into another.
   using Buf = E[2][KT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
-  __shared__ __attribute__((aligned(16))) E own_k[128 * D], own_v[128 * D];
+  __shared__ __attribute__((aligned(16))) E own[2][128 * D];  // keys, values; then sums
   __shared__ __attribute__((aligned(16))) float stat[2][2][KT];
   __shared__ __attribute__((aligned(16))) int2 spans[2][KT];
-  __shared__ uint64_t active[WALK / 64];
+  __shared__ uint64_t active[WALK / 64], partly[WALK / 64];
   __shared__ uint16_t list[WALK];
-  __shared__ float tops[8];
+  __shared__ float2 tops[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = wave >> 2;
   const bool uneven = p.causal || p.spans;
@@ -340,26 +341,27 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
     const Stream<E> vs = {tok_row<E>(p.v, b, 0, kvh), p.v.ts, p.kv_len, p.dim};
 #pragma unroll
     for (int i = 0; i < 128; i += 64) {
-      Copy<E, D, 512, 64>::issue(ks, key0 + i, own_k + i * D, tid);
-      Copy<E, D, 512, 64>::issue(vs, key0 + i, own_v + i * D, tid);
+      Copy<E, D, 512, 64>::issue(ks, key0 + i, own[0] + i * D, tid);
+      Copy<E, D, 512, 64>::issue(vs, key0 + i, own[1] + i * D, tid);
     }
+  }
+  // The masks of the first tiles and the bounds of |ds| are on their way with them;
+  // nothing waits before the first tile is sent for too.
+  int4 early = {0, 0, 0, 0};
+  if (p.tile_spans && tid < q_tiles) early = p.tile_spans[(int64_t)b * q_tiles + tid];
+  if (is_half<E>) {
+    const float2 *qb = (const float2 *)p.q_bound + ((int64_t)b * p.q_heads + kvh * p.share) * q_tiles;
+    float2 top = {0.0f, 0.0f};
+    for (int64_t i = tid; i < (int64_t)p.share * q_tiles; i += 512) {
+      const float2 x = qb[i];
+      top = {fmaxf(top.x, x.x), fmaxf(top.y, x.y)};
+    }
+    top = {wave_fmax(top.x), wave_fmax(top.y)};
+    if (lane == 0) tops[wave] = top;
   }
   int e = 0;
-  if (is_half<E>) {
-    const float *qb = p.q_bound + 2 * ((int64_t)b * p.q_heads + kvh * p.share) * q_tiles;
-    const float g = block_top<512>(qb, (int64_t)p.share * q_tiles, 2, tops);
-    const float d = block_top<512>(qb + 1, (int64_t)p.share * q_tiles, 2, tops);
-    block_copied();
-    float n = 0.0f;
-#pragma unroll
-    for (int k = 0; k < D / 16; k++) {
-      const frag<E> v = lds_rows<E, D>(own_v, 32 * (wave & 3), k, lane);
-#pragma unroll
-      for (int i = 0; i < 8; i++) n = fmaf((float)v[i], (float)v[i], n);
-    }
-    e = headroom(g * sqrtf(other_half(n, false)) + d);
-  }
-  const float ds_by = is_half<E> ? ldexpf(1.0f, e - 15) : 1.0f;
+  float ds_by = 1.0f;
+  bool scaled = !is_half<E>;
 
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
@@ -371,27 +373,25 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
     const int n = min(q_tiles - walk0, WALK), words = (n + 63) >> 6;
     __syncthreads();
     for (int i = tid; i < words * 64; i += 512) {
-      bool act = i < n;
+      bool act = i < n, part = false;
       if (act && p.tile_spans) {
-        const int4 r = p.tile_spans[(int64_t)b * q_tiles + walk0 + i];
+        const int4 r = walk0 + i == tid ? early : p.tile_spans[(int64_t)b * q_tiles + walk0 + i];
         act = r.x < key0 + 128 && r.y > key0;
+        part = r.z > key0 || r.w < min(key0 + 128, p.kv_len);
       }
-      const uint64_t a = __builtin_amdgcn_ballot_w64(act);
-      if (lane == 0) active[i >> 6] = a;
+      const uint64_t a = __builtin_amdgcn_ballot_w64(act), c = __builtin_amdgcn_ballot_w64(part);
+      if (lane == 0) {
+        active[i >> 6] = a;
+        partly[i >> 6] = c;
+      }
     }
     __syncthreads();
     int count = 0;
     for (int w = 0; w < words; w++) {
       const uint64_t a = active[w];
-      if ((w & 7) == wave && a >> lane & 1) {
-        bool part = false;
-        if (p.tile_spans) {
-          const int4 r = p.tile_spans[(int64_t)b * q_tiles + walk0 + 64 * w + lane];
-          part = r.z > key0 || r.w < min(key0 + 128, p.kv_len);
-        }
+      if ((w & 7) == wave && a >> lane & 1)
         list[count + __builtin_popcountll(a & ((1ull << lane) - 1))] =
-            (uint16_t)(64 * w + lane + (part ? 0x8000 : 0));
-      }
+            (uint16_t)(64 * w + lane + (partly[w] >> lane & 1 ? 0x8000 : 0));
       count += __builtin_popcountll(a);
     }
     count = __builtin_amdgcn_readfirstlane(count);
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
     auto tile_at = [&](int i) { return (int)__builtin_amdgcn_readfirstlane(list[i]); };
 
     // Queries, output gradients and row values of tile `t` of head `head`.
-    using Tile = Copy<E, D, 512, KT>;
+    using Tile = Copy<E, D, 512, KT, true>;
     auto load = [&](int t, Buf &to, int in) {
       const int t0 = (walk0 + (t & 0x7fff)) * KT;
       Tile::issue({tok_row<E>(p.q, b, 0, head), p.q.ts, p.q_len, p.dim}, t0, to[0], tid);
@@ -433,6 +433,22 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
     load(now, b0, 0);
     step();
     int next = tile_at(at);
+    if (!scaled) {  // fp16: the power of two for ds of the lane's key
+      scaled = true;
+      block_copied();
+      float2 top = tops[0];
+#pragma unroll
+      for (int w = 1; w < 8; w++) top = {fmaxf(top.x, tops[w].x), fmaxf(top.y, tops[w].y)};
+      float n2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 16; k++) {
+        const frag<E> v = lds_rows<E, D>(own[1], 32 * (wave & 3), k, lane);
+#pragma unroll
+        for (int i = 0; i < 8; i++) n2 = fmaf((float)v[i], (float)v[i], n2);
+      }
+      e = headroom(top.x * sqrtf(other_half(n2, false)) + top.y);
+      ds_by = ldexpf(1.0f, e - 15);
+    }
     // One tile, in buffer `here`; the next one is sent for into `there`.
     auto turn = [&](Buf &here, Buf &there, int in) {
       block_copied();  // this tile is there, and nobody reads the other one any more
@@ -444,9 +460,9 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
       frag<E> x[4][STEPS];
       auto read = [&](int k) {
         x[0][k] = lds_rows<E, D>(q, 32 * half, k, lane);
-        x[1][k] = lds_rows<E, D>(own_k + z, 0, k, lane);
+        x[1][k] = lds_rows<E, D>(own[0] + z, 0, k, lane);
         x[2][k] = lds_rows<E, D>(g, 32 * half, k, lane);
-        x[3][k] = lds_rows<E, D>(own_v + z, 0, k, lane);
+        x[3][k] = lds_rows<E, D>(own[1] + z, 0, k, lane);
       };
       f32x16 w, ds;
 #pragma unroll
@@ -527,53 +543,59 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
   }
   copied<0>();
 
-  // The two halves' sums: the upper waves' through LDS to the lower ones.
-  float *sum = (float *)&b0;  // [128][D / 2 + 4], a half of the elements at a time
+  // The two halves' sums, W columns at a time through LDS: the upper waves' dK goes to
+  // the lower ones, whose dV goes to the upper ones. Chunk c of row r is at c ^ r.
+  constexpr int W = D / 2;
+  const int last = lane + opaque_zero();  // places that take no registers before here
+  const int row = 32 * (wave & 3) + (last & 31);
+  float *sums = (float *)own[0] + row * W;  // [2][128][W]
+  static_assert(2 * 128 * W * sizeof(float) <= sizeof(own), "the sums fit");
+  auto place = [&](int d, int i) { return ((8 * d + acc_row(i, last) / 4) ^ (row & (W / 4 - 1))) * 4; };
+  auto put = [&](const f32x16 (&from)[D / 32], int h, float *to) {
 #pragma unroll
-  for (int h = 0; h < 4; h++) {
+    for (int d = 0; d < D / 64; d++)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const f32x16 x = from[h * (D / 64) + d];
+        *(f32x4 *)(to + place(d, i)) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]};
+      }
+  };
+  auto add = [&](f32x16 (&to)[D / 32], int h, const float *from) {
+#pragma unroll
+    for (int d = 0; d < D / 64; d++)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const f32x4 y = *(const f32x4 *)(from + place(d, i));
+#pragma unroll
+        for (int c = 0; c < 4; c++) to[h * (D / 64) + d][i + c] += y[c];
+      }
+  };
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
     __syncthreads();
-#pragma unroll
-    for (int d = 0; d < D / 64; d++) {
-      f32x16 &x = h < 2 ? dk[(h & 1) * (D / 64) + d] : dv[(h & 1) * (D / 64) + d];
-      float *row = sum + (32 * (wave & 3) + (lane & 31)) * (D / 2 + 4) + 32 * d;
-      if (half)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *(f32x4 *)(row + acc_row(i, lane)) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]};
-    }
+    if (half) put(dk, h, sums);
+    else put(dv, h, sums + 128 * W);
     __syncthreads();
-#pragma unroll
-    for (int d = 0; d < D / 64; d++) {
-      f32x16 &x = h < 2 ? dk[(h & 1) * (D / 64) + d] : dv[(h & 1) * (D / 64) + d];
-      const float *row = sum + (32 * (wave & 3) + (lane & 31)) * (D / 2 + 4) + 32 * d;
-      if (!half)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const f32x4 y = *(const f32x4 *)(row + acc_row(i, lane));
-#pragma unroll
-          for (int c = 0; c < 4; c++) x[i + c] += y[c];
-        }
-    }
+    if (half) add(dv, h, sums + 128 * W);
+    else add(dk, h, sums);
   }
-  if (half) return;
 
-  const float by_k = is_half<E> ? ldexpf(p.scale, -e) : p.scale, by_v = is_half<E> ? 0x1p-15f : 1.0f;
-  if (p.kv_parts > 1) {
-    const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;
-    const int64_t at = (piece * rows + (int64_t)bh * p.kv_len + key) * p.dim;
-    store_part<D>(dk, by_k, p.part_k + at, on, p.dim, lane);
-    store_part<D>(dv, by_v, p.part_v + at, on, p.dim, lane);
-    return;
+  const int64_t rows = (int64_t)p.batch * p.kv_heads * p.kv_len;
+  const int64_t at = (piece * rows + (int64_t)bh * p.kv_len + key) * p.dim;
+  uint32_t again;
+  if (half) {
+    const float by = is_half<E> ? 0x1p-15f : 1.0f;
+    if (p.kv_parts > 1) return store_part<D>(dv, by, p.part_v + at, on, p.dim, lane);
+    again = store_rows<E, D>(dv, by, tok_row<E>(p.dv, b, on ? key : 0, kvh), on, p.dim, lane);
+  } else {
+    const float by = is_half<E> ? ldexpf(p.scale, -e) : p.scale;
+    if (p.kv_parts > 1) return store_part<D>(dk, by, p.part_k + at, on, p.dim, lane);
+    again = store_rows<E, D>(dk, by, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane);
   }
-  uint32_t again =
-      store_rows<E, D>(dk, by_k, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane, 0);
-  again |= store_rows<E, D>(dv, by_v, tok_row<E>(p.dv, b, on ? key : 0, kvh), on, p.dim, lane,
-                            again);
-  if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
   while (again) {
     const int r = __builtin_ctz(again);
     again &= again - 1;
-    redo_key<E>(p, b, kvh, mine0 + r, lane);
+    redo_key<E>(p, b, kvh, mine0 + r, half ? 2 : 1, lane);
   }
 }
 
@@ -608,7 +630,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
 
   float v_top = 0.0f;
   if (is_half<E>)
-    v_top = block_top<256>(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, 1, tops);
+    v_top = block_top<256>(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, tops);
   const float row_lse = on ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
   const float delta = on ? -p.row_delta[(int64_t)bh * p.q_pad + t] : 0.0f;
   frag<E> q[D / 16], g[D / 16];
@@ -718,7 +740,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
     return;
   }
   uint32_t again =
-      store_rows<E, D>(dq, by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim, lane, 0);
+      store_rows<E, D>(dq, by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim, lane);
   if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
   while (again) {
     const int r = __builtin_ctz(again);
@@ -761,7 +783,7 @@ __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
   for (int h = 0; h < 2; h++) {
     if (!(uint32_t)(bits >> (32 * h))) continue;
     const int hb = __shfl(b, 32 * h), hh = __shfl(head, 32 * h), ht = __shfl(t, 32 * h);
-    if (KEYS) redo_key<E>(p, hb, hh, ht, lane);
+    if (KEYS) redo_key<E>(p, hb, hh, ht, 3, lane);
     else redo_query<E>(p, hb, hh, ht, lane);
   }
 }

@@ -160,24 +160,33 @@ struct Stream {
 // in consecutive chunks, so the swizzle is applied to where a lane reads: lanes of
 // a row read all of its chunks, in another order. Bounds as for Stream. The data
 // is there after copied<>() in the issuing wave.
-template <class E, int D, int NT, int R>
+// LEAN: a thread's copies, which must be of rows with the same swizzle, share one offset
+// through a descriptor each, and their places in LDS are scalars: for a kernel without
+// vector registers to spare (where there are, the scalar instructions cost more: 16384
+// tokens, heads of 128, forward 1036 us so and 992 plain).
+template <class E, int D, int NT, int R, bool LEAN = false>
 struct Copy {
   static constexpr int C = D / 8, N = R * C / NT;
   static_assert(R * C % NT == 0, "whole copies");
+  static_assert(!LEAN || NT % (16 * C) == 0, "rows of one swizzle");
 
   static __device__ __forceinline__ void issue(const Stream<E> &m, int row0, E *lds, int tid) {
     const int left = min(m.rows - row0, R);
     const int64_t bytes = left > 0 ? ((int64_t)(left - 1) * m.ts + m.dim) * 2 : 0;
-    auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(m.base + (int64_t)row0 * m.ts), 0,
-                                                  (int)bytes, 0x00020000);
+    const char *base = (const char *)(m.base + (int64_t)row0 * m.ts);
+    const int step = LEAN ? NT / C * (int)m.ts * 2 : 0;
+    const int wave0 = LEAN ? __builtin_amdgcn_readfirstlane(tid) & ~63 : NT > 64 ? tid & ~63 : 0;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int row = NT % C ? (i * NT + tid) / C : i * (NT / C) + tid / C;
-      const int col = (NT % C ? (i * NT + tid) % C : tid % C) ^ swizzle<D>(row);
+      auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(base + (LEAN ? (int64_t)i * step : 0)),
+                                                    0, max((int)bytes - i * step, 0), 0x00020000);
+      const int at_once = LEAN ? tid : i * NT + tid;
+      const int row = NT % C ? at_once / C : (LEAN ? 0 : i * (NT / C)) + tid / C;
+      const int col = (NT % C ? at_once % C : tid % C) ^ swizzle<D>(row);
       // past `dim`: an offset out of every tile's bounds
       const unsigned at = 8 * col < m.dim ? (unsigned)(row * (int)m.ts + 8 * col) * 2u : 0x7fffff00u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, LDS_PTR(void, lds + (i * NT + (NT > 64 ? tid & ~63 : 0)) * 8), 16, at, 0, 0, 0);
+          rsrc, LDS_PTR(void, lds + (i * NT + wave0) * 8), 16, at, 0, 0, 0);
     }
   }
 };
