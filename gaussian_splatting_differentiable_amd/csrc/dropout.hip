@@ -8,7 +8,9 @@
 // element is selected away, not multiplied by 0: its NaN or infinity is gone.
 //
 // Bound: HBM. The generator costs about 100 instructions per four elements (20
-// of them 32-bit multiplies at a quarter of the rate).
+// of them 32-bit multiplies at a quarter of the rate). 32768 x 1024, bf16: 34 us with a
+// residual (201 MB), 31 without (134 MB), partly from the last-level cache; 1535033 x 1,
+// fp32: 4.2 us (12 MB), where the launch is what bounds it.
 #include "tokens_common.h"
 
 namespace {

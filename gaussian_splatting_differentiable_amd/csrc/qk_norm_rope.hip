@@ -14,7 +14,10 @@
 // heads of one token at a time and read its angles and the weights once for
 // them: the angles in 32 bits are twice a 16-bit row's bytes.
 //
-// Bound: HBM (each input read once, each output written once).
+// Bound: HBM (each input read once, each output written once). 2 x 32768 tokens, 16 + 4
+// heads of 128, bf16: 153 us for 671 MB, 4.4 TB/s (a copy reaches 4.7). 3 x 5461 tokens,
+// 12 + 12 heads of 64: forward 25 us (101 MB), backward 34 (151 MB) and the weights'
+// partial sums 5.
 #include "tokens_common.h"
 
 namespace {
