@@ -99,12 +99,14 @@ __device__ __forceinline__ int die_order(int block, int blocks) {
 
 // The dies that share a group of heads: one for each group where the heads divide
 // evenly, else 2, 4 or 8 that take its items in turn.
-inline __host__ __device__ int group_dies(int heads) { return 8 / min(heads & -heads, 8); }
+inline __host__ __device__ int group_dies(int heads) {
+  return heads & 1 ? 8 : heads & 2 ? 4 : heads & 4 ? 2 : 1;
+}
 
 // Workgroups for `parts` of every row tile of every head, a multiple of 8.
 inline int die_blocks(int heads, int tiles, int parts) {
-  const int dies = group_dies(heads);
-  return 8 * (((heads * dies >> 3) * tiles * parts + dies - 1) / dies);
+  const int64_t dies = group_dies(heads), group = heads * dies / 8 * tiles * parts;
+  return (int)(8 * ((group + dies - 1) / dies));
 }
 
 struct Item {
@@ -116,7 +118,7 @@ struct Item {
 // the heads do, from the last tile (causal rows see more keys the later they are) to
 // the first: long blocks come early, and those that a compute unit takes differ.
 __device__ __forceinline__ Item die_item(int block, int heads, int tiles, int parts, bool uneven) {
-  const int dies = group_dies(heads), n = heads * dies >> 3, die = block & 7;
+  const int dies = group_dies(heads), n = (int)((int64_t)heads * dies >> 3), die = block & 7;
   const int at = (block >> 3) * dies + die % dies, whole = at / parts;
   Item x = {-1, 0, at - whole * parts};
   if (whole >= n * tiles) return x;

@@ -15,7 +15,8 @@ hipError_t gs_launch_attn_bwd(AttnK p, int dtype, hipStream_t st);
 
 namespace {
 
-constexpr int64_t LIMIT = (int64_t)1 << 30;     // tokens, heads, batch entries, workgroups
+constexpr int64_t LIMIT = (int64_t)1 << 30;     // tokens, heads, batch entries
+constexpr int64_t THREADS = (int64_t)1 << 32;   // of a launch, never so many
 constexpr int64_t TOKEN_STRIDE = (int64_t)1 << 23;  // 64 rows within 32-bit byte offsets
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -61,9 +62,12 @@ int32_t qk_shape(const gs_qk_shape *s, QkK *k) {
     return GS_ERR_INVALID_ARGUMENT;
   if (s->dim % 8 || s->dim > 256 || s->rot_dim % 8 || s->batch >= LIMIT || s->tokens >= LIMIT ||
       s->q_heads > 65535 || s->k_heads > 65535 ||
-      (int64_t)s->batch * s->tokens >= LIMIT ||
-      (int64_t)s->batch * s->tokens * ((s->q_heads + 3) / 4 + (s->k_heads + 3) / 4) >= LIMIT * 8)
+      (int64_t)s->batch * s->tokens >= LIMIT)
     return GS_ERR_UNSUPPORTED;
+  int lanes = 1;  // of a row of one head
+  while (lanes * 8 < s->dim) lanes *= 2;
+  const int chunks = (s->q_heads + 3) / 4 + (s->k_heads + 3) / 4;
+  if ((int64_t)s->batch * s->tokens * chunks * lanes > THREADS - 256) return GS_ERR_UNSUPPORTED;
   *k = {};
   k->batch = s->batch;
   k->tokens = s->tokens;
@@ -75,8 +79,7 @@ int32_t qk_shape(const gs_qk_shape *s, QkK *k) {
   k->n_positions = s->n_positions;
   k->eps = s->eps;
   k->pos_stride = s->positions_stride;
-  k->lanes = 1;
-  while (k->lanes * 8 < s->dim) k->lanes *= 2;
+  k->lanes = lanes;
   k->blocks = gs_qk_bwd_blocks(s->batch, s->tokens, s->q_heads, s->k_heads, k->lanes);
   return GS_OK;
 }
@@ -111,10 +114,10 @@ int32_t attn_shape(const gs_attn_shape *s, AttnK *p) {
   if (s->dtype == GS_F32 || s->dim % 8 || s->dim > 128 || s->q_heads > 65535 ||
       s->q_tokens >= LIMIT || s->kv_tokens >= LIMIT)
     return GS_ERR_UNSUPPORTED;
-  // workgroups of every launch below (and of its 32-row form)
-  const int64_t bh = (int64_t)s->batch * s->q_heads;
-  if (bh >= LIMIT || bh * ((s->q_tokens + 31) / 32 + 1) >= LIMIT ||
-      bh * ((s->kv_tokens + 63) / 64 + 1) >= LIMIT)
+  // A launch has fewer than 2^32 threads: 512 for every 64 rows of queries and of keys.
+  const int64_t bh = (int64_t)s->batch * s->q_heads, bk = (int64_t)s->batch * s->kv_heads;
+  const int64_t tiles = THREADS / 512 - 64;  // (some are launched past the last one)
+  if (bh >= LIMIT || bh * ((s->q_tokens + 63) / 64) + bk * ((s->kv_tokens + 63) / 64) > tiles)
     return GS_ERR_UNSUPPORTED;
   *p = {};
   p->batch = s->batch;

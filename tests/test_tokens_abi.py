@@ -55,6 +55,23 @@ def test_attention_shapes(tok, kw, status):
     assert L.gs_attention_bwd_workspace_size(s) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(batch=1 << 18, q_heads=32, kv_heads=32, q_tokens=1, kv_tokens=1), dict(batch=1 << 21),
+    dict(batch=1, q_heads=1, kv_heads=1, q_tokens=1, kv_tokens=(1 << 29) + 1)])
+def test_attention_launches_too_large(tok, kw):
+    """More rows than a launch has threads for are refused, not left to the launch."""
+    L, t, s = tok._lib(), _t(tok, t=8), _attn(tok, **kw)
+    assert L.gs_attention(s, t, t, t, None, t, P, P, 1 << 50, None) == UNSUPPORTED
+    assert L.gs_attention_bwd(s, t, t, t, t, None, t, P, t, t, t, P, 1 << 50, None) == UNSUPPORTED
+    assert L.gs_attention_workspace_size(s) == 0
+
+
+def test_qk_launches_too_large(tok):
+    L, t = tok._lib(), _t(tok)
+    s = _qk(tok, batch=1 << 14, tokens=1 << 14, q_heads=8, rot_dim=0)
+    assert L.gs_qk_norm_rope(s, t, t, None, None, None, None, t, t, None) == UNSUPPORTED
+
+
 def test_attention_pointers_strides_and_workspace(tok):
     L, t, s = tok._lib(), _t(tok), _attn(tok)
     big = 1 << 40
