@@ -316,8 +316,7 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[D / 32], float by
 // 128 on 2, bf16: 1990 us, 1105 TFLOP/s of its four products (four waves a block, 32
 // keys each and all rows: 2350 us).
 template <class E, int D>
-__global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
-                                                                       int q_tiles) {
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int q_tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
   // sees that reads of one do not wait for copies into another.
   using Buf = E[2][KT * D];
@@ -424,8 +423,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles,
       if (wave == 4) copy_words(spans_at, (int *)spans[in], lane);
       if (wave == 5) copy_words(spans_at + 64, (int *)spans[in] + 64, lane);
     };
-    // Steps to the next tile; `then` is the one after it, read from the list a turn
-    // before it is needed.
+    // Steps to the tile after `next`, which is read from the list a turn before it is
+    // needed.
     auto step = [&]() {
       if (++at == count) {
         at = 0;

@@ -9,7 +9,7 @@
 // With many rows a wave looks for its largest scores in the first tile only. Later
 // tiles compute p with the reference that is there; if a lane's sum of them passes 2^13
 // (or is NaN), the wave computes the tile's scores again and looks. Measured, 2 x 8192
-// tokens, 16 heads of 64: 690 us, looking at every tile 714; with few rows (2331 tokens,
+// tokens, 16 heads of 64: 670 us, looking at every tile 705; with few rows (2331 tokens,
 // 8 heads of 64) 27 us and 24, there every tile is looked at.
 // p is rounded to the inputs' 16-bit type for the second product, as matrix
 // instructions take it; l sums the unrounded p.
@@ -175,9 +175,9 @@ struct Softmax {
 // Bound by the matrix units, and in short calls by how evenly blocks fall on the
 // compute units: 16384 tokens, 8 heads of 128, bf16: 1010 us, 1090 TFLOP/s. Heads of 65
 // to 96 have a form of 96, of which three blocks fit a compute unit: 6037 tokens in four
-// sequences, 12 heads of 80: 58 us, in the form of 128 73; 2 x 2048 tokens, 12 heads of
-// 80: 61 and 70. 64 rows a wave instead of 32 were slower: 2 x 8192 tokens, 16 heads of
-// 64: 808 us, with 32 714 (the exponentials of heads of 64 take as long as the products).
+// sequences, 12 heads of 80: 55 us, in the form of 128 67; 2 x 2048 tokens, 12 heads of
+// 80: 59 and 70. 64 rows a wave instead of 32 were slower: 2 x 8192 tokens, 16 heads of
+// 64: 808 us, with 32 690 (the exponentials of heads of 64 take as long as the products).
 template <class E, int D>
 __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
@@ -562,8 +562,8 @@ void gs_attn_plan(AttnK *p) {
 
 // Whether blocks of 128 rows are launched twice: with spans, unless there are so many
 // of them that one with two sequences' keys is hidden among the others. Measured, 6037
-// tokens in four sequences, 12 heads of 80 (576 blocks): 78 us with one pass, 58 with
-// two; where no block has rows of two, 56 and 57.
+// tokens in four sequences, 12 heads of 80 (576 blocks): 71 us with one pass, 55 with
+// two; where no block has rows of two, 51 and 52.
 int gs_attn_passes(const AttnK &p) {
   return p.spans && (int64_t)p.batch * p.q_heads * ((p.q_len + 127) / 128) < 4096 ? 2 : 1;
 }
