@@ -117,7 +117,7 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int
 // and rows that see nothing: -inf, which gives p = 0); with masks the rows' spans, and
 // for each 64 queries the keys that some row sees and that all see (lo, hi, in_lo,
 // in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
-// largest |v_j| of each 64 keys. 16 lanes a row. Bound by its bytes: 2 x 4096 queries, 16
+// largest |v_j| of each 64 keys. 16 lanes a row, 8 of up to 64 elements. Bound by its bytes: 2 x 4096 queries, 16
 // heads of 128, bf16, 67 MB: 13 us, and 4 for the rows of few keys below.
 //
 // o was rounded to 16 bits, and D_i of it is off by as much. Beside gradients of many
@@ -128,7 +128,7 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int
 // 720, a chain of loads that the few blocks with such rows wait for.
 constexpr int D_PAIRS = 8;
 
-template <class E>
+template <class E, int LANES>
 __device__ __forceinline__ float pairs_d(const AttnK &p, int b, int head, int t, int2 see,
                                          int j) {
   const int kvh = head / p.share;
@@ -147,16 +147,17 @@ __device__ __forceinline__ float pairs_d(const AttnK &p, int b, int head, int t,
       s = fmaf((float)fq[e], (float)k[e], s);
       dp = fmaf((float)fg[e], (float)v[e], dp);
     }
-    s = group_sum(in ? s : 0.0f, 16) * p.scale_log2 - lse;
-    d = fmaf(__builtin_amdgcn_exp2f(s), group_sum(in ? dp : 0.0f, 16), d);
+    s = group_sum(in ? s : 0.0f, LANES) * p.scale_log2 - lse;
+    d = fmaf(__builtin_amdgcn_exp2f(s), group_sum(in ? dp : 0.0f, LANES), d);
   }
   return d;
 }
 
-template <class E>
+template <class E, int LANES>
 __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_tiles) {
   __shared__ float top[4][2];
-  const int tid = threadIdx.x, lane = tid & 63, j = tid & 15;
+  const int tid = threadIdx.x, lane = tid & 63, j = tid & (LANES - 1);
+  constexpr int AT_ONCE = 256 / LANES;  // rows
   const int q_blocks = p.batch * p.q_heads * q_tiles;
   float m0 = 0.0f, m1 = 0.0f;
   if ((int)blockIdx.x < q_blocks) {
@@ -173,8 +174,8 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
     }
     int few = 0;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int t = qt * KT + 16 * i + (tid >> 4);
+    for (int i = 0; i < KT / AT_ONCE; i++) {
+      const int t = qt * KT + AT_ONCE * i + tid / LANES;
       float d = 0.0f, n = 0.0f;
       if (t < p.q_len && 8 * j < p.dim) {
         const E *g = tok_row<E>(p.d_o, b, t, head) + 8 * j;
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
           n = fmaf(g0[e], g0[e], fmaf(g1[e], g1[e], n));
         }
       }
-      d = group_sum(d, 16);
+      d = group_sum(d, LANES);
       const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
       const int2 see = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
       const bool pairs = see.x < see.y && see.y - see.x <= D_PAIRS;
@@ -199,16 +200,16 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
                             : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
       }
       if (is_half<E>) {
-        m0 = fmaxf(m0, sqrtf(group_sum(n, 16)));
+        m0 = fmaxf(m0, sqrtf(group_sum(n, LANES)));
         m1 = fmaxf(m1, fabsf(d));
       }
     }
     // a loop of its own, not unrolled: registers for one row's pairs, not for four
 #pragma unroll 1
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < KT / AT_ONCE; i++) {
       if (!(few >> i & 1)) continue;
-      const int t = qt * KT + 16 * i + (tid >> 4);
-      const float d = pairs_d<E>(p, b, head, t, row_span(p, b, t), j);
+      const int t = qt * KT + AT_ONCE * i + tid / LANES;
+      const float d = pairs_d<E, LANES>(p, b, head, t, row_span(p, b, t), j);
       if (j == 0) p.row_delta[(int64_t)bh * p.q_pad + t] = -d;
       m1 = fmaxf(m1, fabsf(d));
     }
@@ -216,8 +217,8 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
     const int at = blockIdx.x - q_blocks, bh = at / kv_tiles, jt = at - bh * kv_tiles;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int t = jt * KT + 16 * i + (tid >> 4);
+    for (int i = 0; i < KT / AT_ONCE; i++) {
+      const int t = jt * KT + AT_ONCE * i + tid / LANES;
       float n = 0.0f;
       if (t < p.kv_len && 8 * j < p.dim) {
         const E *v = tok_row<E>(p.v, b, t, head) + 8 * j;
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_
 #pragma unroll
         for (int e = 0; e < 4; e++) n = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], n));
       }
-      m0 = fmaxf(m0, sqrtf(group_sum(n, 16)));
+      m0 = fmaxf(m0, sqrtf(group_sum(n, LANES)));
     }
   }
   if (!is_half<E>) return;
@@ -752,27 +753,36 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
 }
 
 // ------------------------------------------------------------ the parts' sums
-// 32 lanes a row, in the order of the parts: rows of dQ (KEYS 0), or of dK and dV. Bound
+// 32 lanes a row (16 of up to 64 elements), in the order of the parts: rows of dQ (KEYS 0), or of dK and dV. Bound
 // by its bytes: 2 x 4096 keys, 4 heads of 128, two parts, 84 MB: 14 us.
-template <class E, bool KEYS>
+template <class E, bool KEYS, int LANES>
 __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
-  const int lane = threadIdx.x & 63, e = 4 * (lane & 31);
+  const int lane = threadIdx.x & 63, e = 4 * (lane & (LANES - 1));
   const int len = KEYS ? p.kv_len : p.q_len, heads = KEYS ? p.kv_heads : p.q_heads;
   const int parts = KEYS ? p.kv_parts : p.q_parts;
   const int64_t rows = (int64_t)p.batch * heads * len;
-  const int64_t row = (int64_t)block * 8 + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)block * (256 / LANES) + threadIdx.x / LANES;
   const bool on = row < rows && e < p.dim;
-  const int64_t bh = (on ? row : 0) / len;
-  const int t = (int)((on ? row : 0) - bh * len), b = (int)(bh / heads);
-  const int head = (int)(bh - (int64_t)b * heads);
+  const unsigned r = on ? (unsigned)row : 0, bh = r / (unsigned)len;  // (below 2^29)
+  const int t = (int)(r - bh * len), b = (int)(bh / (unsigned)heads), head = (int)(bh - b * heads);
   f32x4 x = 0.0f, y = 0.0f;
   if (on) {
     const float *px = (KEYS ? p.part_k : p.part_q) + row * p.dim + e;
     const float *py = p.part_v + row * p.dim + e;
-#pragma unroll 4
-    for (int i = 0; i < parts; i++) {
-      x += *(const f32x4 *)(px + i * rows * p.dim);
-      if (KEYS) y += *(const f32x4 *)(py + i * rows * p.dim);
+    for (int i = 0; i < parts; i += 2) {  // two parts under way at a time
+      const int64_t at = i * rows * p.dim, next = min(i + 1, parts - 1) * rows * p.dim;
+      const f32x4 x0 = *(const f32x4 *)(px + at), x1 = *(const f32x4 *)(px + next);
+      f32x4 y0 = 0.0f, y1 = 0.0f;
+      if (KEYS) {
+        y0 = *(const f32x4 *)(py + at);
+        y1 = *(const f32x4 *)(py + next);
+      }
+      x += x0;
+      y += y0;
+      if (i + 1 < parts) {
+        x += x1;
+        y += y1;
+      }
     }
     store4(tok_row<E>(KEYS ? p.dk : p.dq, b, t, head) + e, x);
     if (KEYS) store4(tok_row<E>(p.dv, b, t, head) + e, y);
@@ -783,26 +793,26 @@ __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
   const uint64_t bits = __builtin_amdgcn_ballot_w64(nan);
   if (!bits) return;
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
-  for (int h = 0; h < 2; h++) {
-    if (!(uint32_t)(bits >> (32 * h))) continue;
-    const int hb = __shfl(b, 32 * h), hh = __shfl(head, 32 * h), ht = __shfl(t, 32 * h);
+  for (int at = 0; at < 64; at += LANES) {
+    if (!(bits >> at & ((1ull << LANES) - 1))) continue;
+    const int hb = __shfl(b, at), hh = __shfl(head, at), ht = __shfl(t, at);
     if (KEYS) redo_key<E>(p, hb, hh, ht, 3, lane);
     else redo_query<E>(p, hb, hh, ht, lane);
   }
 }
 
-// Both in one launch, a block of 8 rows of either: the first `key_blocks` are keys'.
-template <class E>
+// Both in one launch: the first `key_blocks` are keys'.
+template <class E, int LANES>
 __global__ __launch_bounds__(256) void k_attn_sum(AttnK p, int key_blocks) {
-  if ((int)blockIdx.x < key_blocks) sum_rows<E, true>(p, blockIdx.x);
-  else sum_rows<E, false>(p, blockIdx.x - key_blocks);
+  if ((int)blockIdx.x < key_blocks) sum_rows<E, true, LANES>(p, blockIdx.x);
+  else sum_rows<E, false, LANES>(p, blockIdx.x - key_blocks);
 }
 
 template <class E, int D>
 hipError_t launch(const AttnK &p, hipStream_t st) {
   const int q_tiles = (p.q_len + KT - 1) / KT, kv_tiles = (p.kv_len + KT - 1) / KT;
   const int prep = p.batch * (p.q_heads * q_tiles + (is_half<E> ? p.kv_heads * kv_tiles : 0));
-  if (prep) k_attn_prep<E><<<prep, 256, 0, st>>>(p, q_tiles, kv_tiles);
+  if (prep) k_attn_prep<E, D == 64 ? 8 : 16><<<prep, 256, 0, st>>>(p, q_tiles, kv_tiles);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int k_tiles = (p.kv_len + 127) / 128, tiles = (p.q_len + 127) / 128;
@@ -819,10 +829,13 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  auto blocks_of = [](int64_t rows, int parts) { return parts > 1 ? (int)((rows + 7) / 8) : 0; };
+  constexpr int LANES = D == 64 ? 16 : 32;
+  auto blocks_of = [](int64_t rows, int parts) {
+    return parts > 1 ? (int)((rows * LANES + 255) / 256) : 0;
+  };
   const int keys = blocks_of((int64_t)p.batch * p.kv_heads * p.kv_len, p.kv_parts);
   const int queries = blocks_of((int64_t)p.batch * p.q_heads * p.q_len, p.q_parts);
-  if (keys + queries) k_attn_sum<E><<<keys + queries, 256, 0, st>>>(p, keys);
+  if (keys + queries) k_attn_sum<E, LANES><<<keys + queries, 256, 0, st>>>(p, keys);
   return hipGetLastError();
 }
 

@@ -306,9 +306,10 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   const int part = item % p.splits, rest = item / p.splits;
   const int rt = rest % row_tiles, bh = rest / row_tiles;
   const int b = bh / p.kv_heads, kvh = bh - b * p.kv_heads;
-  const int64_t rows = (int64_t)p.q_len * p.share, r = (int64_t)rt * 32 + (lane & 31);
+  // (below 2^29: 32-bit divisions)
+  const unsigned share = p.share, rows = p.q_len * share, r = rt * 32u + (lane & 31);
   const bool on = r < rows;
-  const int t = on ? (int)(r / p.share) : 0, head = kvh * p.share + (on ? (int)(r % p.share) : 0);
+  const int t = on ? (int)(r / share) : 0, head = kvh * p.share + (on ? (int)(r % share) : 0);
 
   frag<E> q[D / 16];
   const E *row = tok_row<E>(p.q, b, t, head);
@@ -399,9 +400,9 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   __syncthreads();
   // Eight threads a row.
   const int rr = tid >> 3;
-  const int64_t r2 = min((int64_t)rt * 32 + rr, rows - 1);
-  const bool live = (int64_t)rt * 32 + rr < rows;
-  const int t2 = (int)(r2 / p.share), head2 = kvh * p.share + (int)(r2 % p.share);
+  const unsigned r2 = min(rt * 32u + rr, rows - 1);
+  const bool live = rt * 32u + rr < rows;
+  const int t2 = (int)(r2 / share), head2 = kvh * p.share + (int)(r2 % share);
   m = ml[0][0][rr];
   l = ml[0][1][rr];
   const int64_t at_row = ((int64_t)b * p.q_heads + head2) * p.q_len + t2;
@@ -432,8 +433,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
   for (int k = 0; k < 8 && again; k++) {
     if (!(again >> (8 * k) & 0xff)) continue;
-    const int64_t r3 = (int64_t)rt * 32 + wave * 8 + k;
-    redo_row<E>(p, b, kvh * p.share + (int)(r3 % p.share), (int)(r3 / p.share), lane);
+    const unsigned r3 = rt * 32u + wave * 8 + k;
+    redo_row<E>(p, b, kvh * p.share + (int)(r3 % share), (int)(r3 / share), lane);
   }
 }
 
@@ -494,9 +495,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
     o0 = fmaf(sums[i][lane], w, o0);
     o1 = fmaf(sums[i][lane + 64], w, o1);
   }
-  const int64_t bh = row / p.q_len;
-  const int t = (int)(row - bh * p.q_len), b = (int)(bh / p.q_heads);
-  const int head = (int)(bh - (int64_t)b * p.q_heads);
+  const unsigned bh = (unsigned)row / (unsigned)p.q_len;  // (row is below 2^29)
+  const int t = (int)((unsigned)row - bh * p.q_len), b = (int)(bh / (unsigned)p.q_heads);
+  const int head = (int)(bh - (unsigned)b * p.q_heads);
   if (__builtin_amdgcn_ballot_w64(o0 != o0 || o1 != o1)) {
     redo_row<E>(p, b, head, t, lane);
     return;
