@@ -15,9 +15,9 @@
 // them: the angles in 32 bits are twice a 16-bit row's bytes.
 //
 // Bound: HBM (each input read once, each output written once). 2 x 32768 tokens, 16 + 4
-// heads of 128, bf16: 153 us for 671 MB, 4.4 TB/s (a copy reaches 4.7). 3 x 5461 tokens,
-// 12 + 12 heads of 64: forward 25 us (101 MB), backward 34 (151 MB) and the weights'
-// partial sums 5.
+// heads of 128, bf16: 150 us for 671 MB, 4.5 TB/s (a copy reaches 4.7). 3 x 5461 tokens,
+// 12 + 12 heads of 64: forward 24 us (101 MB), backward 33 (151 MB) and the weights'
+// partial sums 4.
 #include "tokens_common.h"
 
 namespace {
@@ -99,15 +99,15 @@ __device__ __forceinline__ float sum8(f32x4 a, f32x4 b) {
 }
 
 template <class E>
-__global__ __launch_bounds__(256) void k_qk_fwd(QkK p, int64_t items) {
+__global__ __launch_bounds__(256) void k_qk_fwd(QkK p, unsigned items) {
   const Lane l = lane_of(p, threadIdx.x);
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
+  const unsigned item = (blockIdx.x * 256u + threadIdx.x) / (unsigned)p.lanes;
   if (item >= items) return;  // whole groups of lanes leave together
   const int qc = (p.q_heads + HC - 1) / HC, kc = (p.k_heads + HC - 1) / HC;
-  const int64_t bt = item / (qc + kc);
+  const unsigned bt = item / (unsigned)(qc + kc);
   const int chunk = (int)(item - bt * (qc + kc));
-  const int64_t b = bt / p.tokens;
-  const int token = (int)(bt - b * p.tokens);
+  const int64_t b = bt / (unsigned)p.tokens;
+  const int token = (int)(bt - (unsigned)b * p.tokens);
   const bool key = chunk >= qc;
   const int h0 = (key ? chunk - qc : chunk) * HC, heads = key ? p.k_heads : p.q_heads;
   const TokK in = key ? p.k : p.q, out = key ? p.ko : p.qo;
@@ -162,10 +162,10 @@ __global__ __launch_bounds__(256) void k_qk_bwd(QkK p) {
   }
   for (int64_t item = (int64_t)blockIdx.x * groups + threadIdx.x / p.lanes; item < items;
        item += (int64_t)gridDim.x * groups) {
-    const int64_t bt = item / chunks;
-    const int h0 = (int)(item - bt * chunks) * HC;
-    const int64_t b = bt / p.tokens;
-    const int token = (int)(bt - b * p.tokens);
+    const unsigned bt = (unsigned)item / (unsigned)chunks;  // (items are below 2^32)
+    const int h0 = (int)((unsigned)item - bt * chunks) * HC;
+    const int64_t b = bt / (unsigned)p.tokens;
+    const int token = (int)(bt - (unsigned)b * p.tokens);
     f32x4 a[HC], c[HC], g0[HC], g1[HC];
 #pragma unroll
     for (int h = 0; h < HC; h++) {
@@ -251,7 +251,7 @@ void launch_fwd(const QkK &p, hipStream_t st) {
   const int chunks = (p.q_heads + HC - 1) / HC + (p.k_heads + HC - 1) / HC;
   const int64_t items = (int64_t)p.batch * p.tokens * chunks;
   const int64_t blocks = (items * p.lanes + 255) / 256;
-  k_qk_fwd<E><<<(unsigned)blocks, 256, 0, st>>>(p, items);
+  k_qk_fwd<E><<<(unsigned)blocks, 256, 0, st>>>(p, (unsigned)items);
 }
 
 }  // namespace
