@@ -513,7 +513,9 @@ typedef struct {
  * rot_dim/2}) or, with neighbours = 1, (z_{2i}, z_{2i+1}) -> (a c - b s,
  * a s + b c); the other elements stay.
  *   dim: a multiple of 8 up to 256, rot_dim a multiple of 8 up to dim (0: no
- *     rotation); other sizes GS_ERR_UNSUPPORTED. dtype: any gs_dtype.
+ *     rotation); batch x tokens below 2^30, and times heads / 4 (of q and of k,
+ *     rounded up) times dim / 8 (up to a power of two) below 2^32; other sizes
+ *     GS_ERR_UNSUPPORTED. dtype: any gs_dtype.
  *   q_heads or k_heads may be 0 (queries or keys alone).
  *   q_weight, k_weight [dim] float or NULL (all ones), 16-byte aligned.
  *   cos_sin [n_positions][rot_dim] float, 16-byte aligned: the rot_dim/2 cosines,
