@@ -280,8 +280,9 @@ int32_t gs_attention_bwd(const gs_attn_shape *shape, const gs_tokens *dL_do, con
   if (p.batch == 0 || (nq == 0 && nk == 0)) return GS_OK;
   if ((nq && !lse) || !aligned(lse, 4)) return GS_ERR_INVALID_ARGUMENT;
   p.lse = (float *)lse;
-  if (workspace_bytes < gs_attention_bwd_workspace_size(shape)) return GS_ERR_WORKSPACE;
-  if (nq && (!workspace || !aligned(workspace, 256))) return GS_ERR_INVALID_ARGUMENT;
+  const size_t need = gs_attention_bwd_workspace_size(shape);
+  if (workspace_bytes < need) return GS_ERR_WORKSPACE;
+  if (need && (!workspace || !aligned(workspace, 256))) return GS_ERR_INVALID_ARGUMENT;
   attn_bwd_layout(&p, spans != nullptr || p.causal, shape->dtype == GS_F16, workspace);
   return hip_status(gs_launch_attn_bwd(p, shape->dtype, (hipStream_t)stream));
 }
