@@ -398,8 +398,9 @@ class QkNormRope(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, cos_sin, positions = ctx.saved_tensors
-        g = qk_norm_rope_bwd(dq.contiguous(), dk.contiguous(), q, k, q_weight, k_weight,
-                             cos_sin=cos_sin, positions=positions, **ctx.how)
+        dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))  # None: was None
+        g = qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, cos_sin=cos_sin,
+                             positions=positions, **ctx.how)
         return (*g, None, None, None, None)
 
 
