@@ -9,7 +9,7 @@ shapes, allocate outputs and workspaces, and enqueue on the current stream (or
 Tensors are ``[batch, tokens, heads, dim]`` with any strides whose innermost is 1
 (views of a joint projection, say). The ``*_bwd`` functions take and return
 gradients explicitly; ``Attention``, ``QkNormRope`` and ``Dropout`` are the same
-calls for autograd.
+calls for autograd (the first two have no second derivative: asking for it is an error).
 """
 from __future__ import annotations
 
@@ -20,6 +20,7 @@ import math
 from struct import Struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import GS_OK, GsError, lib
 
@@ -396,6 +397,7 @@ class QkNormRope(torch.autograd.Function):
                             **ctx.how)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, cos_sin, positions = ctx.saved_tensors
         dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))  # None: was None
@@ -415,6 +417,7 @@ class Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, spans, o, lse = ctx.saved_tensors
         return (*attention_bwd(do.contiguous(), q, k, v, o, lse, spans=spans, **ctx.how),
@@ -433,5 +436,6 @@ class Dropout(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         dy = dy.contiguous()
-        return (dropout(dy, *ctx.how, per_row=ctx.per_row), dy if ctx.residual else None,
+        # the same linear map, seen by autograd: it may be differentiated again
+        return (Dropout.apply(dy, None, *ctx.how, ctx.per_row), dy if ctx.residual else None,
                 None, None, None, None)

@@ -20,40 +20,51 @@ def _norm_bwd(dy, x, w, eps):
     return g[0], g[1] if w is not None else None
 
 
+def _qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=None,
+                  neighbours=False, eps=1e-6):
+    return _norm(q, q_weight, eps), _norm(k, k_weight, eps)
+
+
+def _qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_sin=None,
+                      positions=None, neighbours=False, eps=1e-6):
+    dq, dqw = (None, None) if q is None else _norm_bwd(dq_out, q, q_weight, eps)
+    dk, dkw = (None, None) if k is None else _norm_bwd(dk_out, k, k_weight, eps)
+    return dq, dk, dqw, dkw
+
+
+def _attention(q, k, v, *, spans=None, causal=False, scale=None):
+    s = torch.einsum("bnhd,bmhd->bhnm", q, k) * (1.0 if scale is None else scale)
+    return torch.einsum("bhnm,bmhd->bnhd", torch.softmax(s, 3), v), torch.logsumexp(s, 3)
+
+
+def _attention_bwd(do, q, k, v, o, lse, **how):
+    with torch.enable_grad():
+        xs = [t.detach().requires_grad_() for t in (q, k, v)]
+        y, _ = _attention(*xs, **how)
+    return torch.autograd.grad(y, xs, do)
+
+
+def _dropout(x, p, seed, offset=0, *, residual=None, per_row=False):
+    g = torch.Generator().manual_seed(seed + offset)
+    keep = torch.rand(x.shape[:1] if per_row else x.shape, generator=g) >= p
+    keep = keep.view(-1, *[1] * (x.dim() - 1)) if per_row else keep
+    y = torch.where(keep, x / (1 - p), torch.zeros(()))
+    return y if residual is None else residual + y
+
+
 @pytest.fixture
 def tok(monkeypatch):
+    """The module, its calls stood in for by the formulas, whose inside autograd does not see."""
     from gaussian_splatting_differentiable_amd import tokens
 
-    def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=None,
-                     neighbours=False, eps=1e-6):
-        return _norm(q, q_weight, eps), _norm(k, k_weight, eps)
+    def opaque(f):
+        def call(*args, **kw):
+            with torch.no_grad():
+                return f(*args, **kw)
+        return call
 
-    def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, *, cos_sin=None,
-                         positions=None, neighbours=False, eps=1e-6):
-        dq, dqw = (None, None) if q is None else _norm_bwd(dq_out, q, q_weight, eps)
-        dk, dkw = (None, None) if k is None else _norm_bwd(dk_out, k, k_weight, eps)
-        return dq, dk, dqw, dkw
-
-    def attention(q, k, v, *, spans=None, causal=False, scale=None):
-        s = torch.einsum("bnhd,bmhd->bhnm", q, k) * (1.0 if scale is None else scale)
-        p = torch.softmax(s, 3)
-        return torch.einsum("bhnm,bmhd->bnhd", p, v), torch.logsumexp(s, 3)
-
-    def attention_bwd(do, q, k, v, o, lse, **how):
-        with torch.enable_grad():
-            xs = [t.detach().requires_grad_() for t in (q, k, v)]
-            y, _ = attention(*xs, **how)
-        return torch.autograd.grad(y, xs, do)
-
-    def dropout(x, p, seed, offset=0, *, residual=None, per_row=False):
-        g = torch.Generator().manual_seed(seed + offset)
-        keep = torch.rand(x.shape[:1] if per_row else x.shape, generator=g) >= p
-        keep = keep.view(-1, *[1] * (x.dim() - 1)) if per_row else keep
-        y = torch.where(keep, x / (1 - p), torch.zeros(()))
-        return y if residual is None else residual + y
-
-    for f in (qk_norm_rope, qk_norm_rope_bwd, attention, attention_bwd, dropout):
-        monkeypatch.setattr(tokens, f.__name__, f)
+    for f in (_qk_norm_rope, _qk_norm_rope_bwd, _attention, _attention_bwd, _dropout):
+        monkeypatch.setattr(tokens, f.__name__[1:], opaque(f))
     return tokens
 
 
@@ -72,3 +83,35 @@ def test_queries_or_keys_alone(tok, which):
     y.backward(g)
     want = _norm_bwd(g, x, w, 1e-6)
     assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1])
+
+
+def _square_of_gradient(f, x, w):
+    """|d/dx |f(x w)|^2|^2: w is in it both through f and beside it."""
+    g, = torch.autograd.grad(f(x * w).square().sum(), x, create_graph=True)
+    return g.square().sum()
+
+
+def test_second_derivatives_are_refused_not_dropped(tok):
+    """Attention and the norm have no second derivative: asking for one is an error, where a
+    backward that autograd does not see would leave its terms out of the result."""
+    x, w = _randn(4, 1, 3, 2, 8).requires_grad_(), _randn(5, 8).requires_grad_()
+    k, v = _randn(6, 1, 4, 2, 8), _randn(7, 1, 4, 2, 8)
+    for f in (lambda q: tok.Attention.apply(q, k, v, None, False, None),
+              lambda q: tok.QkNormRope.apply(q, k, None, None, None, None, False, 1e-6)[0]):
+        with pytest.raises(RuntimeError, match="differentiate twice"):
+            _square_of_gradient(f, x, w).backward()
+
+
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_dropout_is_differentiable_twice(tok, per_row, residual):
+    x, w, r = (_randn(i, 5, 7).requires_grad_() for i in (8, 9, 10))
+    rest = (r,) if residual else ()
+
+    def second(f):
+        return torch.autograd.grad(_square_of_gradient(f, x, w), (x, w, *rest))
+
+    got = second(lambda t: tok.Dropout.apply(t, *(rest or (None,)), 0.4, 3, 5, per_row))
+    want = second(lambda t: _dropout(t, 0.4, 3, 5, residual=r if rest else None, per_row=per_row))
+    for a, b in zip(got, want):
+        assert torch.allclose(a, b, rtol=1e-12, atol=1e-12)
