@@ -209,7 +209,7 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, cos_sin=None, positions=
     shape, size, tq, tk, at, dev = _qk_args(q, k, q_weight, k_weight, cos_sin, positions,
                                             neighbours, eps)
     if _elsewhere(stream, dev):
-        with _there(stream, dev, (q, k, q_weight, k_weight, cos_sin, positions)):
+        with _there(stream, dev, (q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)):
             return qk_norm_rope(q, k, q_weight, k_weight, cos_sin=cos_sin, positions=positions,
                                 neighbours=neighbours, eps=eps, q_out=q_out, k_out=k_out)
     q_out = None if q is None else _out("q_out", q_out, q)

@@ -38,3 +38,46 @@ def test_backward_workspace_is_checked_whenever_there_is_one(tok, dtype, nq, nk)
         return
     for ws in (None, C.c_void_p((1 << 20) + 16)):
         assert L.gs_attention_bwd(s, t, t, t, t, None, t, P, t, t, t, ws, need, None) == BAD
+
+
+def test_every_tensor_of_a_call_is_marked_as_used_on_its_stream(tok, monkeypatch):
+    """What the caller gives for outputs too: memory that it drops while the other stream still
+    writes there must not be handed out again."""
+    torch = pytest.importorskip("torch")
+
+    class Left(Exception):
+        pass
+
+    def there(stream, device, tensors):
+        marked.extend(id(t) for t in tensors if t is not None)
+        raise Left
+
+    monkeypatch.setattr(tok, "_elsewhere", lambda stream, device: True)
+    monkeypatch.setattr(tok, "_there", there)
+    monkeypatch.setattr(tok, "_qk_args", lambda *a: (None, 0, None, None, [None] * 4, None))
+    monkeypatch.setattr(tok, "_attn_args", lambda *a: (None, (None, (1, 2, 3), 0, 0)))
+    monkeypatch.setattr(tok, "_DTYPES", {torch.float32: 0})
+
+    def t(*shape):
+        return torch.zeros(*shape)
+
+    class OnDevice:  # dropout looks at its input's device before anything else
+        device, dtype = torch.device("cuda", 0), torch.float32
+
+    x = (1, 3, 2, 8)
+    calls = [
+        (tok.qk_norm_rope, [t(*x), t(*x), t(8), t(8)],
+         dict(cos_sin=t(3, 8), positions=t(3), q_out=t(*x), k_out=t(*x))),
+        (tok.qk_norm_rope_bwd, [t(*x), t(*x), t(*x), t(*x), t(8), t(8)],
+         dict(cos_sin=t(3, 8), positions=t(3))),
+        (tok.attention, [t(*x), t(*x), t(*x)], dict(spans=t(3, 2), out=t(*x), workspace=t(64))),
+        (tok.attention_bwd, [t(*x), t(*x), t(*x), t(*x), t(*x), t(1, 2, 3)],
+         dict(spans=t(3, 2), workspace=t(64))),
+        (tok.dropout, [OnDevice()], dict(p=0.5, seed=1, residual=t(*x), out=t(*x))),
+    ]
+    for call, args, kw in calls:
+        marked = []
+        with pytest.raises(Left):
+            call(*args, **kw, stream=object())
+        for a in args + [v for v in kw.values() if isinstance(v, torch.Tensor)]:
+            assert id(a) in marked, (call.__name__, getattr(a, "shape", a))
