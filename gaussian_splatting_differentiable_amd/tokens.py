@@ -100,6 +100,8 @@ def _base(name, shape, dtype, device):
 
 def _elsewhere(stream, device):
     """Whether a call is not for the current stream of the current device."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {device}")
     return stream is not None or device.index != torch._C._cuda_getDevice()
 
 

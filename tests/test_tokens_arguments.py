@@ -81,3 +81,16 @@ def test_every_tensor_of_a_call_is_marked_as_used_on_its_stream(tok, monkeypatch
             call(*args, **kw, stream=object())
         for a in args + [v for v in kw.values() if isinstance(v, torch.Tensor)]:
             assert id(a) in marked, (call.__name__, getattr(a, "shape", a))
+
+
+def test_a_stream_of_another_device_is_refused(tok):
+    """Its work would otherwise run on the current stream of the tensors' device, unordered with
+    what the caller has on the one that it named."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    assert tok._elsewhere(Stream(), torch.device("cuda", 1))
+    with pytest.raises(ValueError):
+        tok._elsewhere(Stream(), torch.device("cuda", 0))
