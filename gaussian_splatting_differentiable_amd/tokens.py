@@ -189,7 +189,7 @@ def _qk_args(q, k, q_weight, k_weight, cos_sin, positions, neighbours, eps):
     """(shape, workspace bytes, q view, k view, weight, table and position pointers, device)
     after the checks."""
     shape, size = _qk_plan(_about(q), _about(k), _about(q_weight), _about(k_weight),
-                           _about(cos_sin), _about(positions), bool(neighbours), eps)
+                           _about(cos_sin), _about(positions), bool(neighbours), float(eps))
     at = []
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight), ("cos_sin", cos_sin),
                     ("positions", positions)):
@@ -281,7 +281,8 @@ def _attn_args(q, k, v, spans, causal, scale):
             raise ValueError("q: expected [batch, tokens, heads, dim]")
         at, stride = _list2d("spans", spans, q.shape[0], q.shape[1], (2,), q.device)
     return at, _attn_plan(q.shape, k.shape, v.shape, (q.dtype, k.dtype, v.dtype),
-                          (q.device, k.device, v.device), bool(causal), scale, stride)
+                          (q.device, k.device, v.device), bool(causal),
+                          None if scale is None else float(scale), stride)
 
 
 def attention_workspace_size(q, k, *, causal=False, backward=False) -> int:
@@ -394,7 +395,7 @@ class QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, cos_sin, positions, neighbours, eps):
         ctx.save_for_backward(q, k, q_weight, k_weight, cos_sin, positions)
-        ctx.how = dict(neighbours=neighbours, eps=eps)
+        ctx.how = dict(neighbours=neighbours, eps=float(eps))  # as it is now
         return qk_norm_rope(q, k, q_weight, k_weight, cos_sin=cos_sin, positions=positions,
                             **ctx.how)
 
@@ -413,9 +414,9 @@ class Attention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, spans, causal, scale):
-        o, lse = attention(q, k, v, spans=spans, causal=causal, scale=scale)
+        ctx.how = dict(causal=causal, scale=None if scale is None else float(scale))  # as it is now
+        o, lse = attention(q, k, v, spans=spans, **ctx.how)
         ctx.save_for_backward(q, k, v, spans, o, lse)
-        ctx.how = dict(causal=causal, scale=scale)
         return o
 
     @staticmethod

@@ -94,3 +94,33 @@ def test_a_stream_of_another_device_is_refused(tok):
     assert tok._elsewhere(Stream(), torch.device("cuda", 1))
     with pytest.raises(ValueError):
         tok._elsewhere(Stream(), torch.device("cuda", 0))
+
+
+def test_a_scale_or_eps_that_changes_in_place_is_read_at_every_call(tok):
+    """What a call keeps for its sizes is kept by their values, not by the object that held one."""
+    torch = pytest.importorskip("torch")
+
+    class Tensor:
+        device, dtype = torch.device("cuda", 0), torch.bfloat16
+
+        def __init__(self, *shape):
+            self.shape = torch.Size(shape)
+
+        def dim(self):
+            return len(self.shape)
+
+        def stride(self):
+            return (1 << 12, 1 << 8, self.shape[-1], 1)
+
+        def data_ptr(self):
+            return 1 << 20
+
+    x = Tensor(1, 3, 2, 64)
+    for number in (torch.tensor(0.5), __import__("numpy").array(0.5)):
+        a = tok._attn_args(x, x, x, None, False, number)[1][0]
+        e = tok._qk_args(x, x, None, None, None, None, False, number)[0]
+        number += 0.25
+        b = tok._attn_args(x, x, x, None, False, number)[1][0]
+        f = tok._qk_args(x, x, None, None, None, None, False, number)[0]
+        assert tok._ATTN.unpack(a)[8] == tok._QK.unpack(e)[9] == 0.5
+        assert tok._ATTN.unpack(b)[8] == tok._QK.unpack(f)[9] == 0.75

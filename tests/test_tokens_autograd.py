@@ -115,3 +115,17 @@ def test_dropout_is_differentiable_twice(tok, per_row, residual):
     want = second(lambda t: _dropout(t, 0.4, 3, 5, residual=r if rest else None, per_row=per_row))
     for a, b in zip(got, want):
         assert torch.allclose(a, b, rtol=1e-12, atol=1e-12)
+
+
+def test_a_scale_that_changes_between_forward_and_backward(tok):
+    """The backward belongs to the forward that was made."""
+    q, k, v = (_randn(i, 1, 3, 2, 8).requires_grad_() for i in (11, 12, 13))
+    scale, eps = torch.tensor(0.5, dtype=torch.float64), torch.tensor(0.25, dtype=torch.float64)
+    y = tok.Attention.apply(q, k, v, None, False, scale)
+    a, _ = tok.QkNormRope.apply(q, None, None, None, None, None, False, eps)
+    scale += 1.0
+    eps += 1.0
+    got = torch.autograd.grad(y.sum() + a.square().sum(), q)[0]
+    y, _ = _attention(q, k, v, scale=0.5)
+    want = torch.autograd.grad(y.sum() + _norm(q, None, 0.25).square().sum(), q)[0]
+    assert torch.allclose(got, want, rtol=1e-12, atol=1e-12)
