@@ -389,6 +389,13 @@ def dropout(x, p, seed, offset=0, *, residual=None, per_row=False, out=None, str
 
 # ------------------------------------------------------------------ autograd
 
+def _no_gradient(ctx, **at):
+    """Refuses a backward for arguments (name: place) that want a gradient and would get none."""
+    for name, i in at.items():
+        if ctx.needs_input_grad[i]:
+            raise ValueError(f"{name}: no gradient is computed for it (detach it)")
+
+
 class QkNormRope(torch.autograd.Function):
     """QkNormRope.apply(q, k, q_weight, k_weight, cos_sin, positions, neighbours, eps)."""
 
@@ -402,6 +409,7 @@ class QkNormRope(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
+        _no_gradient(ctx, cos_sin=4, eps=7)
         q, k, q_weight, k_weight, cos_sin, positions = ctx.saved_tensors
         dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))  # None: was None
         g = qk_norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, cos_sin=cos_sin,
@@ -422,6 +430,7 @@ class Attention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
+        _no_gradient(ctx, scale=5)
         q, k, v, spans, o, lse = ctx.saved_tensors
         return (*attention_bwd(do.contiguous(), q, k, v, o, lse, spans=spans, **ctx.how),
                 None, None, None)

@@ -129,3 +129,27 @@ def test_a_scale_that_changes_between_forward_and_backward(tok):
     y, _ = _attention(q, k, v, scale=0.5)
     want = torch.autograd.grad(y.sum() + _norm(q, None, 0.25).square().sum(), q)[0]
     assert torch.allclose(got, want, rtol=1e-12, atol=1e-12)
+
+
+def test_what_gets_no_gradient_may_not_want_one(tok):
+    """A learned table, eps or scale would stay as it is without a word."""
+    x, table = _randn(14, 1, 3, 2, 8).requires_grad_(), _randn(15, 3, 8)
+    number = torch.tensor(0.5, dtype=torch.float64)
+
+    def norm(table, eps):
+        return tok.QkNormRope.apply(x, None, None, None, table, None, False, eps)
+
+    def attention(scale):
+        return tok.Attention.apply(x, x, x, None, False, scale)
+
+    wants = table.clone().requires_grad_(), number.clone().requires_grad_()
+    for call, arg, want in ((lambda t: norm(t, 1e-6), table, wants[0]),
+                            (lambda t: norm(None, t), number, wants[1]),
+                            (attention, number, wants[1])):
+        y = call(arg)
+        (y[0] if isinstance(y, tuple) else y).sum().backward()
+        y = call(want)
+        with pytest.raises(ValueError, match="no gradient"):
+            (y[0] if isinstance(y, tuple) else y).sum().backward()
+        with torch.no_grad():
+            call(want)
