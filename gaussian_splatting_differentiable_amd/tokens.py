@@ -144,6 +144,7 @@ def _out(name, out, like):
     if out is None:
         return torch.empty_like(like, memory_format=torch.contiguous_format)
     _same(name, out, like.shape, like.dtype, like.device)
+    torch.autograd.graph.increment_version(out)  # autograd sees that it is overwritten
     return out
 
 

@@ -153,3 +153,17 @@ def test_what_gets_no_gradient_may_not_want_one(tok):
             (y[0] if isinstance(y, tuple) else y).sum().backward()
         with torch.no_grad():
             call(want)
+
+
+def test_an_output_that_overwrites_what_autograd_saved_is_noticed(tok):
+    """An output that the caller gives is written like any in-place result."""
+    base = _randn(16, 3, 4)
+    w = _randn(17, 4).requires_grad_()
+    for part in (base, base[1:]):
+        y = (base * w).sum()
+        assert tok._out("out", part, part) is part  # as every call takes its outputs
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():
+        x = torch.zeros(3)
+        assert tok._out("out", x, x) is x
