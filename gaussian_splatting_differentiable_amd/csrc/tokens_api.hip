@@ -111,8 +111,10 @@ int32_t attn_shape(const gs_attn_shape *s, AttnK *p) {
       (s->causal != 0 && s->causal != 1) || !isfinite(s->scale) || !(s->scale > 0.0f) ||
       s->spans_stride < 0)
     return GS_ERR_INVALID_ARGUMENT;
+  // (lse / scale, where the backward's scores start, and scale log2 e stay within 32 bits)
   if (s->dtype == GS_F32 || s->dim % 8 || s->dim > 128 || s->q_heads > 65535 ||
-      s->q_tokens >= LIMIT || s->kv_tokens >= LIMIT)
+      s->q_tokens >= LIMIT || s->kv_tokens >= LIMIT || s->scale < 0x1p-100f ||
+      s->scale > 0x1p100f)
     return GS_ERR_UNSUPPORTED;
   // A launch has fewer than 2^32 threads: 512 for every 64 rows of queries and of keys.
   const int64_t bh = (int64_t)s->batch * s->q_heads, bk = (int64_t)s->batch * s->kv_heads;

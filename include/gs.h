@@ -552,8 +552,8 @@ int32_t gs_qk_norm_rope_bwd(const gs_qk_shape *shape, const gs_tokens *dL_dq_out
  * lse_i = log sum_j exp s_ij, o_i = sum_j exp(s_ij - lse_i) v_j. Query heads
  * h * (q_heads / kv_heads) .. share key head h.
  *   dtype GS_BF16 or GS_F16 (GS_F32: GS_ERR_UNSUPPORTED); dim a multiple of 8
- *     up to 128; scale > 0; fewer than 2^29 rows (batch x heads x tokens in whole
- *     64s, of queries and keys together).
+ *     up to 128; scale > 0, from 2^-100 to 2^100 (others: GS_ERR_UNSUPPORTED); fewer
+ *     than 2^29 rows (batch x heads x tokens in whole 64s, of queries and keys together).
  *   o, lse and the gradients <- may not overlap an input or each other.
  *   spans: int32 pairs [lo, hi) of the keys a query sees, pair b * spans_stride +
  *     t for query t (stride 0: one list for the batch), 8-byte aligned, or NULL:

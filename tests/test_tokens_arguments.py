@@ -17,7 +17,7 @@ def tok():
 
 
 P = C.c_void_p(1 << 20)
-BAD = -1
+BAD, UNSUPPORTED = -1, -5
 
 
 def _attn(tok, **kw):
@@ -124,3 +124,16 @@ def test_a_scale_or_eps_that_changes_in_place_is_read_at_every_call(tok):
         f = tok._qk_args(x, x, None, None, None, None, False, number)[0]
         assert tok._ATTN.unpack(a)[8] == tok._QK.unpack(e)[9] == 0.5
         assert tok._ATTN.unpack(b)[8] == tok._QK.unpack(f)[9] == 0.75
+
+
+def test_scales_whose_log_sums_leave_32_bits_are_refused(tok):
+    """The backward starts its scores from -lse / scale, the forward multiplies by scale log2 e:
+    both stay finite for scales from 2^-100 to 2^100."""
+    L, t = tok._lib(), tok._TOKENS.pack(1 << 20, 1 << 23, 512, 64)
+    for scale in (2.0 ** -101, 1e-38, 1e-45, 2.0 ** 101, 3e38):
+        s = _attn(tok, scale=scale)
+        assert L.gs_attention(s, t, t, t, None, t, P, P, 1 << 40, None) == UNSUPPORTED
+        assert L.gs_attention_bwd(s, t, t, t, t, None, t, P, t, t, t, P, 1 << 40, None) == UNSUPPORTED
+        assert L.gs_attention_bwd_workspace_size(s) == 0
+    for scale in (2.0 ** -100, 2.0 ** 100):
+        assert L.gs_attention_bwd_workspace_size(_attn(tok, scale=scale)) > 0
