@@ -14,8 +14,11 @@
 // p and ds are rounded to the inputs' 16-bit type for the products, which makes dq's and
 // dk's error 1.45 to 1.6 times that of rounding the results alone. Probabilities
 // of long rows fall below the normal range of fp16 (2^-14), so for fp16 the
-// kernels work on p 2^15 and on ds 2^e with e from a bound on |ds|
-// (|do_i| |v_j| + |D_i|), powers of two that are taken out of the 32-bit sums.
+// kernels work on p 2^15 and on ds 2^e, powers of two that are taken out of the 32-bit
+// sums. e is each key's own in dK and each query's in dQ, and falls as the largest |ds| of
+// the pairs that are seen does not fit: what masked pairs hold, and the gradients of other
+// sequences in a row, do not matter. (8192 tokens, fp16, forward and backward, against e from
+// a bound of all |do| |v| + |D|: 8 heads of 64 745 us for 721, of 128 on 2 1217 for 1205.)
 #include "attention_common.h"
 
 namespace {
@@ -27,10 +30,16 @@ constexpr bool is_half = false;
 template <>
 constexpr bool is_half<f16_t> = true;
 
-// 2^e with |ds| 2^e < 2^14 for |ds| <= bound.
-__device__ __forceinline__ int headroom(float bound) {
-  if (!(bound > 0.0f) || bound > 3e38f) return 0;
-  return max(-100, min(100, 13 - ilogbf(bound)));
+// The powers of two that ds 2^e starts with: more than any result of fp16 shows, and far
+// from 2^128 where ds is largest (|do . v| and |D| are below 2^40).
+constexpr int DS_POWERS = 60;
+
+// The powers of two that ds 2^e of a lane's own row has too many where its largest
+// magnitude is `top` (both halves' lanes of the row together): then 2^10 is left, which
+// keeps 2^24 below it in fp16's normal numbers, and later ones may be 32 times as large.
+__device__ __forceinline__ int too_many(float top) {
+  top = other_half(top, true);
+  return top >= 32768.0f && top <= 3e38f ? ilogbf(top) - 10 : 0;
 }
 
 // ------------------------------------------------------------ rows done again
@@ -116,8 +125,7 @@ __device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int
 // The rows' values as dK and dV start from them, in whole tiles (rows past the end
 // and rows that see nothing: -inf, which gives p = 0); with masks the rows' spans, and
 // for each 64 queries the keys that some row sees and that all see (lo, hi, in_lo,
-// in_hi); for fp16 the largest |do_i| and |D_i| of each 64 queries and the
-// largest |v_j| of each 64 keys. 16 lanes a row, 8 of up to 64 elements. Bound by its bytes: 2 x 4096 queries, 16
+// in_hi). 16 lanes a row, 8 of up to 64 elements. Bound by its bytes: 2 x 4096 queries, 16
 // heads of 128, bf16, 67 MB: 13 us, and 4 for the rows of few keys below.
 //
 // o was rounded to 16 bits, and D_i of it is off by as much. Beside gradients of many
@@ -154,116 +162,53 @@ __device__ __forceinline__ float pairs_d(const AttnK &p, int b, int head, int t,
 }
 
 template <class E, int LANES>
-__global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles, int kv_tiles) {
-  __shared__ float top[4][2];
+__global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles) {
   const int tid = threadIdx.x, lane = tid & 63, j = tid & (LANES - 1);
   constexpr int AT_ONCE = 256 / LANES;  // rows
-  const int q_blocks = p.batch * p.q_heads * q_tiles;
-  float m0 = 0.0f, m1 = 0.0f;
-  if ((int)blockIdx.x < q_blocks) {
-    const int bh = blockIdx.x / q_tiles, qt = blockIdx.x - bh * q_tiles;
-    const int b = bh / p.q_heads, head = bh - b * p.q_heads;
-    if (p.tile_spans && head == 0 && tid < 64) {
-      const int t = qt * KT + lane;
-      const int2 s = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
-      const bool on = t < p.q_len, some = s.x < s.y;
-      const int4 r = {wave_min(some ? s.x : INT32_MAX), wave_max(s.y), wave_max(on ? s.x : 0),
-                      wave_min(on ? s.y : INT32_MAX)};
-      if (lane == 0) p.tile_spans[(int64_t)b * q_tiles + qt] = r;
-      p.row_spans[(int64_t)b * p.q_pad + t] = s;
-    }
-    int few = 0;
+  const int bh = blockIdx.x / q_tiles, qt = blockIdx.x - bh * q_tiles;
+  const int b = bh / p.q_heads, head = bh - b * p.q_heads;
+  if (p.tile_spans && head == 0 && tid < 64) {
+    const int t = qt * KT + lane;
+    const int2 s = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
+    const bool on = t < p.q_len, some = s.x < s.y;
+    const int4 r = {wave_min(some ? s.x : INT32_MAX), wave_max(s.y), wave_max(on ? s.x : 0),
+                    wave_min(on ? s.y : INT32_MAX)};
+    if (lane == 0) p.tile_spans[(int64_t)b * q_tiles + qt] = r;
+    p.row_spans[(int64_t)b * p.q_pad + t] = s;
+  }
+  int few = 0;
 #pragma unroll
-    for (int i = 0; i < KT / AT_ONCE; i++) {
-      const int t = qt * KT + AT_ONCE * i + tid / LANES;
-      float d = 0.0f, n = 0.0f;
-      if (t < p.q_len && 8 * j < p.dim) {
-        const E *g = tok_row<E>(p.d_o, b, t, head) + 8 * j;
-        const E *o = tok_row<E>(p.o, b, t, head) + 8 * j;
-        const f32x4 g0 = load4(g), g1 = load4(g + 4), o0 = load4(o), o1 = load4(o + 4);
+  for (int i = 0; i < KT / AT_ONCE; i++) {
+    const int t = qt * KT + AT_ONCE * i + tid / LANES;
+    float d = 0.0f;
+    if (t < p.q_len && 8 * j < p.dim) {
+      const E *g = tok_row<E>(p.d_o, b, t, head) + 8 * j;
+      const E *o = tok_row<E>(p.o, b, t, head) + 8 * j;
+      const f32x4 g0 = load4(g), g1 = load4(g + 4), o0 = load4(o), o1 = load4(o + 4);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          d = fmaf(g0[e], o0[e], fmaf(g1[e], o1[e], d));
-          n = fmaf(g0[e], g0[e], fmaf(g1[e], g1[e], n));
-        }
-      }
-      d = group_sum(d, LANES);
-      const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
-      const int2 see = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
-      const bool pairs = see.x < see.y && see.y - see.x <= D_PAIRS;
-      few |= (int)pairs << i;
-      if (j == 0) {
-        const int64_t at = (int64_t)bh * p.q_pad + t;
-        if (!pairs) p.row_delta[at] = -d;
-        p.row_lse[at] = lse == -INFINITY
-                            ? -INFINITY
-                            : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
-      }
-      if (is_half<E>) {
-        m0 = fmaxf(m0, sqrtf(group_sum(n, LANES)));
-        m1 = fmaxf(m1, fabsf(d));
-      }
+      for (int e = 0; e < 4; e++) d = fmaf(g0[e], o0[e], fmaf(g1[e], o1[e], d));
     }
-    // a loop of its own, not unrolled: registers for one row's pairs, not for four
+    d = group_sum(d, LANES);
+    const float lse = t < p.q_len ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
+    const int2 see = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
+    const bool pairs = see.x < see.y && see.y - see.x <= D_PAIRS;
+    few |= (int)pairs << i;
+    if (j == 0) {
+      const int64_t at = (int64_t)bh * p.q_pad + t;
+      if (!pairs) p.row_delta[at] = -d;
+      p.row_lse[at] = lse == -INFINITY
+                          ? -INFINITY
+                          : ((is_half<E> ? 15.0f * ATTN_LN2 : 0.0f) - lse) / p.scale;
+    }
+  }
+  // a loop of its own, not unrolled: registers for one row's pairs, not for four
 #pragma unroll 1
-    for (int i = 0; i < KT / AT_ONCE; i++) {
-      if (!(few >> i & 1)) continue;
-      const int t = qt * KT + AT_ONCE * i + tid / LANES;
-      const float d = pairs_d<E, LANES>(p, b, head, t, row_span(p, b, t), j);
-      if (j == 0) p.row_delta[(int64_t)bh * p.q_pad + t] = -d;
-      m1 = fmaxf(m1, fabsf(d));
-    }
-  } else {
-    const int at = blockIdx.x - q_blocks, bh = at / kv_tiles, jt = at - bh * kv_tiles;
-    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
-#pragma unroll
-    for (int i = 0; i < KT / AT_ONCE; i++) {
-      const int t = jt * KT + AT_ONCE * i + tid / LANES;
-      float n = 0.0f;
-      if (t < p.kv_len && 8 * j < p.dim) {
-        const E *v = tok_row<E>(p.v, b, t, head) + 8 * j;
-        const f32x4 v0 = load4(v), v1 = load4(v + 4);
-#pragma unroll
-        for (int e = 0; e < 4; e++) n = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], n));
-      }
-      m0 = fmaxf(m0, sqrtf(group_sum(n, LANES)));
-    }
+  for (int i = 0; i < KT / AT_ONCE; i++) {
+    if (!(few >> i & 1)) continue;
+    const int t = qt * KT + AT_ONCE * i + tid / LANES;
+    const float d = pairs_d<E, LANES>(p, b, head, t, row_span(p, b, t), j);
+    if (j == 0) p.row_delta[(int64_t)bh * p.q_pad + t] = -d;
   }
-  if (!is_half<E>) return;
-  m0 = wave_fmax(m0);
-  m1 = wave_fmax(m1);
-  if (lane == 0) {
-    top[tid >> 6][0] = m0;
-    top[tid >> 6][1] = m1;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < 4; w++) {
-      m0 = fmaxf(m0, top[w][0]);
-      m1 = fmaxf(m1, top[w][1]);
-    }
-    if ((int)blockIdx.x < q_blocks) {
-      p.q_bound[2 * (int64_t)blockIdx.x] = m0;
-      p.q_bound[2 * (int64_t)blockIdx.x + 1] = m1;
-    } else {
-      p.v_bound[blockIdx.x - q_blocks] = m0;
-    }
-  }
-}
-
-// Largest of n floats at x, by a block of NT threads.
-template <int NT>
-__device__ __forceinline__ float block_top(const float *x, int n, float *lds) {
-  float m = 0.0f;
-  for (int i = threadIdx.x; i < n; i += NT) m = fmaxf(m, x[i]);
-  m = wave_fmax(m);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = lds[0];
-#pragma unroll
-  for (int w = 1; w < NT / 64; w++) m = fmaxf(m, lds[w]);
-  return m;
 }
 
 // Stores a transposed accumulator (lane: a row, registers: its elements) and
@@ -327,7 +272,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
   __shared__ __attribute__((aligned(16))) int2 spans[2][KT];
   __shared__ uint64_t active[WALK / 64], partly[WALK / 64];
   __shared__ uint16_t list[WALK];
-  __shared__ float2 tops[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = wave >> 2;
   const bool uneven = p.causal || p.spans;
@@ -348,23 +292,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
       Copy<E, D, 512, 64>::issue(vs, key0 + i, own[1] + i * D, tid);
     }
   }
-  // The masks of the first tiles and the bounds of |ds| are on their way with them;
-  // nothing waits before the first tile is sent for too.
+  // The masks of the first tiles are on their way with them; nothing waits before the
+  // first tile is sent for too.
   int4 early = {0, 0, 0, 0};
   if (p.tile_spans && tid < q_tiles) early = p.tile_spans[(int64_t)b * q_tiles + tid];
-  if (is_half<E>) {
-    const float2 *qb = (const float2 *)p.q_bound + ((int64_t)b * p.q_heads + kvh * p.share) * q_tiles;
-    float2 top = {0.0f, 0.0f};
-    for (int64_t i = tid; i < (int64_t)p.share * q_tiles; i += 512) {
-      const float2 x = qb[i];
-      top = {fmaxf(top.x, x.x), fmaxf(top.y, x.y)};
-    }
-    top = {wave_fmax(top.x), wave_fmax(top.y)};
-    if (lane == 0) tops[wave] = top;
-  }
-  int e = 0;
-  float ds_by = 1.0f;
-  bool scaled = !is_half<E>;
+  int e = is_half<E> ? DS_POWERS : 0;  // of ds of the lane's key, whose p has 15 already
+  float ds_by = ldexpf(1.0f, e - 15);
 
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
@@ -436,22 +369,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
     load(now, b0, 0);
     step();
     int next = tile_at(at);
-    if (!scaled) {  // fp16: the power of two for ds of the lane's key
-      scaled = true;
-      block_copied();
-      float2 top = tops[0];
-#pragma unroll
-      for (int w = 1; w < 8; w++) top = {fmaxf(top.x, tops[w].x), fmaxf(top.y, tops[w].y)};
-      float n2 = 0.0f;
-#pragma unroll
-      for (int k = 0; k < D / 16; k++) {
-        const frag<E> v = lds_rows<E, D>(own[1], 32 * (wave & 3), k, lane);
-#pragma unroll
-        for (int i = 0; i < 8; i++) n2 = fmaf((float)v[i], (float)v[i], n2);
-      }
-      e = headroom(top.x * sqrtf(other_half(n2, false)) + top.y);
-      ds_by = ldexpf(1.0f, e - 15);
-    }
     // One tile, in buffer `here`; the next one is sent for into `there`.
     auto turn = [&](Buf &here, Buf &there, int in) {
       block_copied();  // this tile is there, and nobody reads the other one any more
@@ -515,6 +432,20 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
         ds[i] *= w[i];
         if (is_half<E>) ds[i] *= ds_by;
       }
+      if (is_half<E>) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(ds[i]));
+        if (__builtin_amdgcn_ballot_w64(top >= 32768.0f)) {
+          const int down = too_many(top);
+          const float by = ldexpf(1.0f, -down);
+          e -= down;
+          ds_by *= by;
+          ds *= by;
+#pragma unroll
+          for (int d = 0; d < D / 32; d++) dk[d] *= by;
+        }
+      }
       frag<E> pw[2], pd[2];
 #pragma unroll
       for (int k = 0; k < 2; k++) {
@@ -545,6 +476,11 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
     }
   }
   copied<0>();
+  if (is_half<E>) {  // the halves have powers of their own
+    const float by = ldexpf(1.0f, -e);
+#pragma unroll
+    for (int d = 0; d < D / 32; d++) dk[d] *= by;
+  }
 
   // The two halves' sums, W columns at a time through LDS: the upper waves' dK goes to
   // the lower ones, whose dV goes to the upper ones. Chunk c of row r is at c ^ r.
@@ -591,9 +527,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
     if (p.kv_parts > 1) return store_part<D>(dv, by, p.part_v + at, on, p.dim, lane);
     again = store_rows<E, D>(dv, by, tok_row<E>(p.dv, b, on ? key : 0, kvh), on, p.dim, lane);
   } else {
-    const float by = is_half<E> ? ldexpf(p.scale, -e) : p.scale;
-    if (p.kv_parts > 1) return store_part<D>(dk, by, p.part_k + at, on, p.dim, lane);
-    again = store_rows<E, D>(dk, by, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane);
+    if (p.kv_parts > 1) return store_part<D>(dk, p.scale, p.part_k + at, on, p.dim, lane);
+    again = store_rows<E, D>(dk, p.scale, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane);
   }
   while (again) {
     const int r = __builtin_ctz(again);
@@ -609,11 +544,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
 // 1370 us, 1200 TFLOP/s of its three products. Heads of 65 to 96 have a form of 96 (2 x 2048 queries,
 // 12 heads of 80, bf16: 74 us, in the form of 128 90).
 template <class E, int D>
-__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int kv_tiles) {
+__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles) {
   using Buf = E[2][KT * D];
   __shared__ __attribute__((aligned(16))) Buf b0, b1;
   __shared__ int2 range[4];
-  __shared__ float tops[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int once = gridDim.x / p.passes, pass = blockIdx.x / once;
   const Item it = die_item(blockIdx.x % once, p.batch * p.q_heads, tiles, p.q_parts,
@@ -631,25 +565,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
     if (__syncthreads_count(on) == 0) return;
   }
 
-  float v_top = 0.0f;
-  if (is_half<E>)
-    v_top = block_top<256>(p.v_bound + ((int64_t)b * p.kv_heads + kvh) * kv_tiles, kv_tiles, tops);
   const float row_lse = on ? p.lse[(int64_t)bh * p.q_len + t] : -INFINITY;
   const float delta = on ? -p.row_delta[(int64_t)bh * p.q_pad + t] : 0.0f;
   frag<E> q[D / 16], g[D / 16];
   const E *qr = tok_row<E>(p.q, b, on ? t : 0, head), *gr = tok_row<E>(p.d_o, b, on ? t : 0, head);
-  float norm = 0.0f;
 #pragma unroll
   for (int k = 0; k < D / 16; k++) {
     const int chunk = 2 * k + (lane >> 5);
     q[k] = row_operand<E>(qr, chunk, on && 8 * chunk < p.dim);
     g[k] = row_operand<E>(gr, chunk, on && 8 * chunk < p.dim);
-    if (is_half<E>)
-#pragma unroll
-      for (int i = 0; i < 8; i++) norm = fmaf((float)g[k][i], (float)g[k][i], norm);
   }
-  const int e = is_half<E> ? headroom(sqrtf(other_half(norm, false)) * v_top + fabsf(delta)) : 0;
-  const float lse = row_lse == -INFINITY ? INFINITY : row_lse * ATTN_LOG2E - (float)e;
+  int e = is_half<E> ? DS_POWERS : 0;  // of ds of the lane's query
+  float lse = row_lse == -INFINITY ? INFINITY : row_lse * ATTN_LOG2E - (float)e;
   const bool some = span.x < span.y;
   const int lo = __builtin_amdgcn_readfirstlane(wave_min(some ? span.x : INT32_MAX));
   const int hi = __builtin_amdgcn_readfirstlane(wave_max(span.y));
@@ -720,6 +647,20 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles, int k
         for (int i = 0; i < 16; i++) {
           const int key = key0 + 32 * s + acc_row(i, lane);
           if ((unsigned)(key - span.x) >= (unsigned)(span.y - span.x)) ds[i] = 0.0f;
+        }
+      }
+      if (is_half<E>) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(ds[i]));
+        if (__builtin_amdgcn_ballot_w64(top >= 32768.0f)) {
+          const int down = too_many(top);
+          const float by = ldexpf(1.0f, -down);
+          e -= down;
+          lse += (float)down;
+          ds *= by;
+#pragma unroll
+          for (int d = 0; d < D / 32; d++) dq[d] *= by;
         }
       }
 #pragma unroll
@@ -810,9 +751,9 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnK p, int key_blocks) {
 
 template <class E, int D>
 hipError_t launch(const AttnK &p, hipStream_t st) {
-  const int q_tiles = (p.q_len + KT - 1) / KT, kv_tiles = (p.kv_len + KT - 1) / KT;
-  const int prep = p.batch * (p.q_heads * q_tiles + (is_half<E> ? p.kv_heads * kv_tiles : 0));
-  if (prep) k_attn_prep<E, D == 64 ? 8 : 16><<<prep, 256, 0, st>>>(p, q_tiles, kv_tiles);
+  const int q_tiles = (p.q_len + KT - 1) / KT;
+  if (q_tiles)
+    k_attn_prep<E, D == 64 ? 8 : 16><<<p.batch * p.q_heads * q_tiles, 256, 0, st>>>(p, q_tiles);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int k_tiles = (p.kv_len + 127) / 128, tiles = (p.q_len + 127) / 128;
@@ -824,8 +765,8 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
   }
   if (tiles) {
     const int blocks = die_blocks(p.batch * p.q_heads, tiles, p.q_parts) * p.passes;
-    if (D == 128 && p.dim <= 96) k_attn_bwd_q<E, 96><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
-    else k_attn_bwd_q<E, D><<<blocks, 256, 0, st>>>(p, tiles, kv_tiles);
+    if (D == 128 && p.dim <= 96) k_attn_bwd_q<E, 96><<<blocks, 256, 0, st>>>(p, tiles);
+    else k_attn_bwd_q<E, D><<<blocks, 256, 0, st>>>(p, tiles);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }

@@ -148,8 +148,8 @@ size_t attn_layout(AttnK *p, void *ws) {
   return o + round256(slots * 8);
 }
 
-size_t attn_bwd_layout(AttnK *p, bool masked, bool half, void *ws) {
-  const size_t qt = (p->q_len + 63) / 64, kt = (p->kv_len + 63) / 64, b = p->batch;
+size_t attn_bwd_layout(AttnK *p, bool masked, void *ws) {
+  const size_t qt = (p->q_len + 63) / 64, b = p->batch;
   char *at = (char *)ws;
   size_t total = 0;
   auto part = [&](size_t bytes) {
@@ -163,8 +163,6 @@ size_t attn_bwd_layout(AttnK *p, bool masked, bool half, void *ws) {
   p->row_spans = (int2 *)part(masked ? b * p->q_pad * 8 : 0);
   char *spans = part(masked ? b * qt * 16 : 0);
   p->tile_spans = masked ? (int4 *)spans : nullptr;
-  p->q_bound = (float *)part(half ? b * p->q_heads * qt * 8 : 0);
-  p->v_bound = (float *)part(half ? b * p->kv_heads * kt * 4 : 0);
   gs_attn_bwd_plan(p, masked);
   const size_t q = b * p->q_heads * p->q_len * p->dim * 4, k = b * p->kv_heads * p->kv_len * p->dim * 4;
   p->part_q = (float *)part(p->q_parts > 1 ? q * p->q_parts : 0);
@@ -245,9 +243,8 @@ size_t gs_attention_bwd_workspace_size(const gs_attn_shape *shape) {
   if (attn_shape(shape, &p) != GS_OK) return 0;
   // with spans or without: the larger
   AttnK n = p;
-  const bool half = shape->dtype == GS_F16;
-  const size_t a = attn_bwd_layout(&p, true, half, nullptr);
-  const size_t c = attn_bwd_layout(&n, false, half, nullptr);
+  const size_t a = attn_bwd_layout(&p, true, nullptr);
+  const size_t c = attn_bwd_layout(&n, false, nullptr);
   return a > c ? a : c;
 }
 
@@ -285,7 +282,7 @@ int32_t gs_attention_bwd(const gs_attn_shape *shape, const gs_tokens *dL_do, con
   const size_t need = gs_attention_bwd_workspace_size(shape);
   if (workspace_bytes < need) return GS_ERR_WORKSPACE;
   if (need && (!workspace || !aligned(workspace, 256))) return GS_ERR_INVALID_ARGUMENT;
-  attn_bwd_layout(&p, spans != nullptr || p.causal, shape->dtype == GS_F16, workspace);
+  attn_bwd_layout(&p, spans != nullptr || p.causal, workspace);
   return hip_status(gs_launch_attn_bwd(p, shape->dtype, (hipStream_t)stream));
 }
 

@@ -98,7 +98,6 @@ struct AttnK {
   float *row_lse, *row_delta;  // [batch][q_heads][q_pad]: -lse / scale (fp16: less 15 bits), -D_i
   int2 *row_spans;             // [batch][q_pad]: spans as the masks leave them
   int4 *tile_spans;
-  float *q_bound, *v_bound;
   int q_parts, kv_parts;
   float *part_q, *part_k, *part_v;
 };

@@ -1,0 +1,110 @@
+"""The token operators where results must not depend on what they do not see and at the ends of
+their ranges, against the formulas in 64 bits."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import token_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+def _tokens():
+    from gaussian_splatting_differentiable_amd import tokens
+    return tokens
+
+
+def _randn(seed, *shape, dtype=BF, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+
+
+def _inputs(seed, B, nq, nk, H, Hk, d, dtype):
+    return (_randn(seed, B, nq, H, d, dtype=dtype, scale=1.5), _randn(seed + 1, B, nk, Hk, d, dtype=dtype),
+            _randn(seed + 2, B, nk, Hk, d, dtype=dtype), _randn(seed + 3, B, nq, H, d, dtype=dtype))
+
+
+def _run(q, k, v, do, **how):
+    tok = _tokens()
+    o, lse = tok.attention(q, k, v, **how)
+    dq, dk, dv = tok.attention_bwd(do, q, k, v, o, lse, **how)
+    torch.cuda.synchronize()
+    return dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+
+
+def _compare(q, k, v, do, spans=None, causal=False, scale=None):
+    allowed = ref.spans_of(q.shape[1], k.shape[1], spans, causal)
+    want = ref.attention(q, k, v, allowed, scale or 1 / math.sqrt(q.shape[3]), do)
+    got = _run(q, k, v, do, spans=spans, causal=causal, scale=scale)
+    for n, x in got.items():
+        ref.check(n, x, want[n])
+
+
+def _list(*parts):
+    """Spans of packed parts: (rows, lo, hi) each."""
+    return torch.cat([torch.tensor([[lo, hi]], dtype=torch.int32).expand(n, 2)
+                      for n, lo, hi in parts]).contiguous().cuda()
+
+
+# ------------------------------------------------- fp16 gradients and what is not seen
+
+def _lifted(seed, n, nk, H, Hk, d, lift):
+    """Inputs whose q is `lift` times larger and k smaller: the scores are the same, and dk (or
+    with 1 / lift dq) stays above fp16's smallest numbers where do is small."""
+    q, k, v, do = _inputs(seed, 1, n, nk, H, Hk, d, FP)
+    return q * lift, k / lift, v, do
+
+
+@pytest.mark.parametrize("bad", [6e4, math.inf, math.nan])
+@pytest.mark.parametrize("end", [1536, 1500])
+@pytest.mark.parametrize("d,lift", [(64, 64.0), (64, 1 / 64), (128, 64.0), (128, 1 / 64)])
+def test_small_gradients_beside_masked_places_in_fp16(bad, end, d, lift):
+    """Padding in tiles of its own (1536) or inside one (1500), with gradients of 2^-17 beside."""
+    q, k, v, do = _lifted(1, 1600, 1600, 2, 1, d, lift)
+    do *= 2.0 ** -17
+    for t in (q, k, v, do):
+        t[:, end:] = bad
+    _compare(q, k, v, do, spans=_list((end, 0, end), (1600 - end, 0, 0)))
+
+
+@pytest.mark.parametrize("where", [64, 16383])
+@pytest.mark.parametrize("bad", [6e4, math.inf])
+def test_small_gradients_of_a_long_cache_with_a_masked_value_in_fp16(where, bad):
+    """The value is in a tile that the queries see the rest of, or in one that none sees."""
+    q, k, v, do = _lifted(2, 33, 16384, 1, 1, 64, 1 / 64)
+    v[:, where] = bad
+    spans = _list((33, 65, 16384)) if where == 64 else _list((33, 0, 16320))
+    _compare(q, k, v, do * 2.0 ** -14, spans=spans)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("lift", [64.0, 1 / 64])
+def test_sequences_of_different_gradient_scales_in_fp16(d, lift):
+    """Two packed sequences whose gradients are 2^22 apart, then their values 2^11."""
+    q, k, v, do = _lifted(3, 1500, 1500, 2, 2, d, lift)
+    do[:, :700] *= 2.0 ** -17
+    do[:, 700:] *= 2.0 ** 5
+    spans = _list((700, 0, 700), (800, 700, 1500))
+    _compare(q, k, v, do, spans=spans)
+    v[:, 700:] *= 2.0 ** 11
+    do[:, 700:] *= 2.0 ** -16
+    _compare(q, k, v, do, spans=spans)
+
+
+def test_gradients_that_grow_and_shrink_along_the_tokens_in_fp16():
+    """|do| over 2^16 from query to query and |v| over 2^8 from key to key, both ways (no result
+    leaves fp16's range)."""
+    for sign in (1, -1):
+        q, k, v, do = _inputs(4, 1, 900, 900, 2, 1, 64, FP)
+        ramp = 2.0 ** (sign * torch.linspace(-8, 8, 900, device="cuda"))[None, :, None, None]
+        v = (v.float() * ramp.sqrt()).to(FP)
+        do = (do.float() * ramp).to(FP)
+        for causal in (False, True):
+            allowed = ref.spans_of(900, 900, None, causal)
+            want = ref.attention(q, k, v, allowed, 0.125, do)
+            assert all(float(want[n][0].abs().max()) < 65504 for n in ("o", "dq", "dk", "dv"))
+            _compare(q, k, v, do, causal=causal)
