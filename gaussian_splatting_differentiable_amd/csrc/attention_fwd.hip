@@ -5,10 +5,13 @@
 // One pass over the keys with a running reference m_i and sum l_i (32 bits, in
 // powers of two): p = 2^(s - m), o and l scaled by 2^(m - m') when the reference
 // moves. It moves only when some score of the wave passes it by 8 (rounding is
-// relative, so p above 1 are as exact as those below).
+// relative, so p above 1 are as exact as those below). In fp16 p below 2^-14 lose bits and
+// below 2^-25 count as 0, which many keys add up: there the reference is taken 5 below the
+// largest score and moves when one passes it by 10, so that p is off by 2^-30 of the row's
+// largest at most.
 // With many rows a wave looks for its largest scores in the first tile only. Later
 // tiles compute p with the reference that is there; if a lane's sum of them passes 2^13
-// (or is NaN), the wave computes the tile's scores again and looks. Measured, 2 x 8192
+// (fp16: 2^15; or is NaN), the wave computes the tile's scores again and looks. Measured, 2 x 8192
 // tokens, 16 heads of 64: 670 us, looking at every tile 705; with few rows (2331 tokens,
 // 8 heads of 64) 27 us and 24, there every tile is looked at.
 // p is rounded to the inputs' 16-bit type for the second product, as matrix
@@ -55,8 +58,17 @@ __device__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
         l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
 }
 
-// Largest sum of a lane's p of a tile that needs no look: each of them fits fp16.
-constexpr float P_ROOM = 8192.0f;
+// How far the reference is below the largest score when it moves, and how far a score may
+// pass it, in powers of two; and the largest sum of a lane's p of a tile that needs no look:
+// that of its 32 p as large as a look leaves them, each of which fits the type.
+template <class E>
+struct Room {
+  static constexpr float BELOW = 0.0f, PASS = 8.0f, SUM = 0x1p13f;
+};
+template <>
+struct Room<f16_t> {
+  static constexpr float BELOW = 5.0f, PASS = 10.0f, SUM = 0x1p15f;
+};
 
 // A wave's running softmax over its 32 rows and its share of o.
 template <class E, int D>
@@ -127,8 +139,8 @@ struct Softmax {
 #pragma unroll
           for (int i = 0; i < 16; i++) top = fmaxf(top, s[b][i]);
         top = other_half(top, true) * scale_log2;
-        if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
-          const float to = fmaxf(m, top), ref = to == -INFINITY ? 0.0f : to;
+        if (__builtin_amdgcn_ballot_w64(top > m + Room<E>::PASS)) {
+          const float to = fmaxf(m, top - Room<E>::BELOW), ref = to == -INFINITY ? 0.0f : to;
           const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
           m = to;
           l *= shrink;
@@ -145,7 +157,7 @@ struct Softmax {
           s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], scale_log2, -ref));
           sum += s[b][i];
         }
-      if (look || !__builtin_amdgcn_ballot_w64(!(sum <= P_ROOM))) break;
+      if (look || !__builtin_amdgcn_ballot_w64(!(sum <= Room<E>::SUM))) break;
       look = true;
     }
     l += sum;

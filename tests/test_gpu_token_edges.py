@@ -108,3 +108,20 @@ def test_gradients_that_grow_and_shrink_along_the_tokens_in_fp16():
             want = ref.attention(q, k, v, allowed, 0.125, do)
             assert all(float(want[n][0].abs().max()) < 65504 for n in ("o", "dq", "dk", "dv"))
             _compare(q, k, v, do, causal=causal)
+
+
+@pytest.mark.parametrize("nq,H", [(3, 1), (300, 64)])
+def test_small_probabilities_of_a_long_row_in_fp16(nq, H):
+    """One key holds nearly all of a row's probability, and 2^17 others 2^-26 of it each, which
+    together are 2^-9: more than the result's rounding. Off by at most 2^-30 of the largest for
+    each key (half the smallest number of fp16, and the 32-fold that p is held at)."""
+    n = 1 << 17
+    q = torch.zeros(1, nq, H, 64, dtype=FP, device="cuda")
+    k = torch.zeros(1, n, 1, 64, dtype=FP, device="cuda")
+    v = torch.ones(1, n, 1, 64, dtype=FP, device="cuda")
+    q[..., 0], k[:, 77, :, 0], v[:, 77] = 4.0, 4.5, 0.0
+    o, lse = _tokens().attention(q, k, v, scale=1.0)
+    small = (n - 1) * math.exp(-18.0)
+    want, room = small / (1 + small), n * 2.0 ** -30 + 4 * 2.0 ** -11 * small
+    assert float((o.double() - want).abs().max()) <= room
+    assert float((lse.double() - (18.0 + math.log1p(small))).abs().max()) <= 1e-5 * 18
