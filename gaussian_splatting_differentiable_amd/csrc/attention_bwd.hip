@@ -25,11 +25,6 @@ namespace {
 
 constexpr int WALK = 4096;  // streamed query tiles whose masks a block holds at a time
 
-template <class E>
-constexpr bool is_half = false;
-template <>
-constexpr bool is_half<f16_t> = true;
-
 // The powers of two that ds 2^e starts with: more than any result of fp16 shows, and far
 // from 2^128 where ds is largest (|do . v| and |D| are below 2^40).
 constexpr int DS_POWERS = 60;
@@ -43,19 +38,18 @@ __device__ __forceinline__ int too_many(float top) {
 }
 
 // ------------------------------------------------------------ rows done again
-// As in the forward: a gradient row that holds a NaN is computed again from its
-// own (query, key) pairs alone, since 0 x NaN from masked pairs may have spoilt it.
 
 template <class E>
-__device__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
+__device__ __forceinline__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
   const int2 span = row_span(p, b, t);
   const int kvh = head / p.share;
-  const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
+  const int64_t bh = (int64_t)b * p.q_heads + head;
   const E *q = tok_row<E>(p.q, b, t, head), *g = tok_row<E>(p.d_o, b, t, head);
-  const float lse = p.lse[at] * ATTN_LOG2E;
-  const float delta = -p.row_delta[((int64_t)b * p.q_heads + head) * p.q_pad + t];
-  float a0 = 0.0f, a1 = 0.0f;
-  for (int j0 = span.x; j0 < span.y; j0 += 64) {
+  const float lse = p.lse[bh * p.q_len + t] * ATTN_LOG2E, delta = -p.row_delta[bh * p.q_pad + t];
+  RowSum dq;
+  bool open = true;
+#pragma unroll 1
+  for (int j0 = span.x; open && j0 < span.y; j0 += 64) {
     const int n = min(64, span.y - j0);
     float ds = 0.0f;
     if (lane < n) {
@@ -63,62 +57,70 @@ __device__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
       ds = __builtin_amdgcn_exp2f(s - lse) *
            (dot_row(g, tok_row<E>(p.v, b, j0 + lane, kvh), p.dim) - delta);
     }
-    for (int j = 0; j < n; j++) {
-      const E *k = tok_row<E>(p.k, b, j0 + j, kvh);
-      const float w = __shfl(ds, j);
-      if (lane < p.dim) a0 = fmaf(w, (float)k[lane], a0);
-      if (lane + 64 < p.dim) a1 = fmaf(w, (float)k[lane + 64], a1);
-    }
+    open = dq.add<E>(ds, first_bits(n), p.k, b, kvh, j0, span.y - 1, p.dim, lane);
   }
-  E *o = tok_row<E>(p.dq, b, t, head);
-  if (lane < p.dim) o[lane] = (E)(a0 * p.scale);
-  if (lane + 64 < p.dim) o[lane + 64] = (E)(a1 * p.scale);
+  dq.store(tok_row<E>(p.dq, b, t, head), p.scale, p.dim, lane);
 }
 
-// which: 1 dK, 2 dV, 3 both.
+// One key's row of dV, or of dK.
 template <class E>
-__device__ void redo_key(const AttnK &p, int b, int kvh, int key, int which, int lane) {
+__device__ __forceinline__ void redo_key(const AttnK &p, int b, int kvh, int key, bool of_v, int lane) {
   const E *k = tok_row<E>(p.k, b, key, kvh), *v = tok_row<E>(p.v, b, key, kvh);
-  float k0 = 0.0f, k1 = 0.0f, v0 = 0.0f, v1 = 0.0f;
+  const TokK x = of_v ? p.d_o : p.q;
+  RowSum sum;
+  bool open = true;
+#pragma unroll 1
   for (int head = kvh * p.share; head < (kvh + 1) * p.share; head++)
-    for (int t0 = 0; t0 < p.q_len; t0 += 64) {
+#pragma unroll 1
+    for (int t0 = 0; open && t0 < p.q_len; t0 += 64) {
       const int t = t0 + lane;
       const int2 span = t < p.q_len ? row_span(p, b, t) : make_int2(0, 0);
       const bool in = key >= span.x && key < span.y;
-      uint64_t todo = __builtin_amdgcn_ballot_w64(in);
-      if (!todo) continue;
-      float w = 0.0f, ds = 0.0f;
+      const uint64_t seen = __builtin_amdgcn_ballot_w64(in);
+      if (!seen) continue;
+      float w = 0.0f;
       if (in) {
-        const int64_t at = ((int64_t)b * p.q_heads + head) * p.q_len + t;
+        const int64_t bh = (int64_t)b * p.q_heads + head;
         const float s = dot_row(tok_row<E>(p.q, b, t, head), k, p.dim) * p.scale_log2;
-        w = __builtin_amdgcn_exp2f(s - p.lse[at] * ATTN_LOG2E);
-        ds = w * (dot_row(tok_row<E>(p.d_o, b, t, head), v, p.dim) +
-                  p.row_delta[((int64_t)b * p.q_heads + head) * p.q_pad + t]);
+        w = __builtin_amdgcn_exp2f(s - p.lse[bh * p.q_len + t] * ATTN_LOG2E);
+        if (!of_v)
+          w *= dot_row(tok_row<E>(p.d_o, b, t, head), v, p.dim) + p.row_delta[bh * p.q_pad + t];
       }
-      while (todo) {
-        const int j = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        const E *q = tok_row<E>(p.q, b, t0 + j, head), *g = tok_row<E>(p.d_o, b, t0 + j, head);
-        const float wj = __shfl(w, j), sj = __shfl(ds, j);
-        if (lane < p.dim) {
-          k0 = fmaf(sj, (float)q[lane], k0);
-          v0 = fmaf(wj, (float)g[lane], v0);
-        }
-        if (lane + 64 < p.dim) {
-          k1 = fmaf(sj, (float)q[lane + 64], k1);
-          v1 = fmaf(wj, (float)g[lane + 64], v1);
-        }
+      open = sum.add<E>(w, seen, x, b, head, t0, p.q_len - 1, p.dim, lane);
+    }
+  sum.store(tok_row<E>(of_v ? p.dv : p.dk, b, key, kvh), of_v ? 1.0f : p.scale, p.dim, lane);
+}
+
+// Whether the output gradients (for dV; else the queries) hold a row that spoils among those
+// of the tiles that the block of 128 keys from `block` on was multiplied with and that do not
+// see all of the n keys from `key` on; for dV in fp16 also among those that do.
+template <class E>
+__device__ __forceinline__ bool queries_spoil(const AttnK &p, int b, int kvh, int block, int key,
+                                              int n, bool of_v, int lane) {
+  const bool all = is_half<E> && of_v;
+  const TokK x = of_v ? p.d_o : p.q;
+  if (!p.tile_spans && !all) return false;
+  const int q_tiles = p.q_pad / KT, key_end = min(key + n, p.kv_len);
+#pragma unroll 1
+  for (int i0 = 0; i0 < q_tiles; i0 += 64) {
+    bool at = i0 + lane < q_tiles;
+    if (at && p.tile_spans) {
+      const int4 r = p.tile_spans[(int64_t)b * q_tiles + i0 + lane];
+      at = r.x < block + 128 && r.y > block && (all || r.z > key || r.w < key_end);
+    }
+    for (uint64_t todo = __builtin_amdgcn_ballot_w64(at); todo; todo &= todo - 1) {
+      const int t = (i0 + __builtin_ctzll(todo)) * KT + lane;
+      const bool on = t < p.q_len;
+      const int2 s = on ? row_span(p, b, t) : make_int2(0, 0);
+      const bool seen = s.x <= key && s.y >= key_end;
+#pragma unroll 1
+      for (int head = kvh * p.share; head < (kvh + 1) * p.share; head++) {
+        const bool bad = on && (all || !seen) && row_spoils(tok_row<E>(x, b, t, head), p.dim, seen);
+        if (__builtin_amdgcn_ballot_w64(bad)) return true;
       }
     }
-  E *dk = tok_row<E>(p.dk, b, key, kvh), *dv = tok_row<E>(p.dv, b, key, kvh);
-  if (which & 1) {
-    if (lane < p.dim) dk[lane] = (E)(k0 * p.scale);
-    if (lane + 64 < p.dim) dk[lane + 64] = (E)(k1 * p.scale);
   }
-  if (which & 2) {
-    if (lane < p.dim) dv[lane] = (E)v0;
-    if (lane + 64 < p.dim) dv[lane + 64] = (E)v1;
-  }
+  return false;
 }
 
 // ------------------------------------------------------------ preparation
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(256) void k_attn_prep(AttnK p, int q_tiles) {
 }
 
 // Stores a transposed accumulator (lane: a row, registers: its elements) and
-// returns the rows (bits 0..31) that hold a NaN and were not stored.
+// returns the rows (bits 0..31) that hold a NaN.
 template <class E, int D>
 __device__ __forceinline__ uint32_t store_rows(const f32x16 (&acc)[D / 32], float by, E *row,
                                                bool on, int dim, int lane) {
@@ -222,8 +224,7 @@ __device__ __forceinline__ uint32_t store_rows(const f32x16 (&acc)[D / 32], floa
 #pragma unroll
     for (int i = 0; i < 16; i++) nan |= acc[d][i] != acc[d][i];
   const uint64_t bits = __builtin_amdgcn_ballot_w64(on && nan);
-  const uint32_t skip = (uint32_t)bits | (uint32_t)(bits >> 32);
-  if (on && !(skip >> (lane & 31) & 1)) {
+  if (on) {
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
@@ -233,7 +234,7 @@ __device__ __forceinline__ uint32_t store_rows(const f32x16 (&acc)[D / 32], floa
         if (e < dim) store4(row + e, (f32x4){x[i] * by, x[i + 1] * by, x[i + 2] * by, x[i + 3] * by});
       }
   }
-  return skip;
+  return (uint32_t)bits | (uint32_t)(bits >> 32);
 }
 
 // The same into one part's 32-bit sums, which k_attn_sum adds and looks over.
@@ -530,10 +531,14 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
     if (p.kv_parts > 1) return store_part<D>(dk, p.scale, p.part_k + at, on, p.dim, lane);
     again = store_rows<E, D>(dk, p.scale, tok_row<E>(p.dk, b, on ? key : 0, kvh), on, p.dim, lane);
   }
+  if (!again) return;
+  const AttnK &c = args_again();
+  if (!queries_spoil<E>(c, b, kvh, key0, mine0, 32, half, lane)) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the stores above come first
   while (again) {
     const int r = __builtin_ctz(again);
     again &= again - 1;
-    redo_key<E>(p, b, kvh, mine0 + r, half ? 2 : 1, lane);
+    redo_key<E>(c, b, kvh, mine0 + r, half, lane);
   }
 }
 
@@ -685,11 +690,17 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles) {
   }
   uint32_t again =
       store_rows<E, D>(dq, by, tok_row<E>(p.dq, b, on ? t : 0, head), on, p.dim, lane);
-  if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
+  // (with a log sum or a D that is NaN all of dq is, of a query that sees any key)
+  again &= ~(uint32_t)__builtin_amdgcn_ballot_w64(some && (lse != lse || delta != delta));
+  if (!again) return;
+  const AttnK &c = args_again();
+  const int4 see = {lo, hi, in_lo, in_hi};
+  if (!keys_spoil<E, KT, false>(c, c.k, b, kvh, see, lane)) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the stores above come first
   while (again) {
     const int r = __builtin_ctz(again);
     again &= again - 1;
-    redo_query<E>(p, b, head, tile0 + wave * 32 + r, lane);
+    redo_query<E>(c, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
@@ -733,12 +744,36 @@ __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
   for (int i = 0; i < 4; i++) nan |= x[i] != x[i] || y[i] != y[i];
   const uint64_t bits = __builtin_amdgcn_ballot_w64(nan);
   if (!bits) return;
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // the stores above come first
-  for (int at = 0; at < 64; at += LANES) {
-    if (!(bits >> at & ((1ull << LANES) - 1))) continue;
-    const int hb = __shfl(b, at), hh = __shfl(head, at), ht = __shfl(t, at);
-    if (KEYS) redo_key<E>(p, hb, hh, ht, 3, lane);
-    else redo_query<E>(p, hb, hh, ht, lane);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the stores above come first
+  const AttnK &c = args_again();
+  const int most = KEYS ? 128 : 32;  // rows that a block's waves, or a wave, took together
+  int until = 0;
+  bool spoilt[2] = {false, false};  // of dK and dV, or of dQ
+#pragma unroll 1
+  for (int i = 0; i < 64; i += LANES) {
+    if (!(bits >> i & ((1ull << LANES) - 1))) continue;
+    const int hb = __builtin_amdgcn_readlane(b, i), hh = __builtin_amdgcn_readlane(head, i);
+    const int ht = __builtin_amdgcn_readlane(t, i), first = ht / most * most;
+    if (i >= until) {  // the rows of this wave from here on that were taken together
+      const int n = min(min((64 - i) / LANES, first + most - ht), (KEYS ? c.kv_len : c.q_len) - ht);
+      until = i + n * LANES;
+      if (KEYS) {
+        spoilt[0] = queries_spoil<E>(c, hb, hh, first, ht, n, false, lane);
+        spoilt[1] = queries_spoil<E>(c, hb, hh, first, ht, n, true, lane);
+      } else {
+        const int4 s = rows_see(c, hb, first, min(most, c.q_len - first), lane);
+        spoilt[0] = keys_spoil<E, KT, false>(c, c.k, hb, hh / c.share, s, lane);
+      }
+    }
+    if (KEYS) {
+      if (spoilt[0]) redo_key<E>(c, hb, hh, ht, false, lane);
+      if (spoilt[1]) redo_key<E>(c, hb, hh, ht, true, lane);
+    } else if (spoilt[0]) {
+      const int64_t bh = (int64_t)hb * c.q_heads + hh;
+      const float lse = c.lse[bh * c.q_len + ht], delta = c.row_delta[bh * c.q_pad + ht];
+      const int2 s = row_span(c, hb, ht);
+      if (s.x >= s.y || (lse == lse && delta == delta)) redo_query<E>(c, hb, hh, ht, lane);
+    }
   }
 }
 

@@ -272,13 +272,159 @@ __device__ __forceinline__ int acc_row(int i, int lane) {
   return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
 }
 
+// ---- rows done again. 0 x NaN and 0 x infinity are NaN: in a matrix product, a row of a
+// masked pair that is not finite spoils results that do not see it; and in fp16 a p that
+// rounds to 0 those that see an infinity. A result with a NaN is therefore computed again
+// from its own pairs in 32 bits, by one wave: but only where there is such a row (else the
+// NaN is its own), and not on once all of it is NaN. 2048 tokens, 8 heads of 64, bf16, one
+// value row with a NaN that is seen, forward and backward: 0.1 ms, as without it (every NaN
+// computed again: 7.2 ms); where two sequences that share a block meet, 0.6 (they are
+// latency: about 3.5 us for 64 pairs of a row).
+
+template <class E>
+inline constexpr bool is_half = false;
+template <>
+inline constexpr bool is_half<f16_t> = true;
+
+// The kernel's arguments (its first), read again where this is called: code that hardly ever
+// runs then keeps none of them in registers while the rest of the kernel does.
+__device__ __forceinline__ const AttnK &args_again() {
+  auto at = (const __attribute__((address_space(4))) AttnK *)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const AttnK *)at;
+}
+
+// Whether a row can spoil results that it is multiplied into by 0: it is not finite, or,
+// with `seen` (by all of them), infinite.
+template <class E>
+__device__ __forceinline__ bool row_spoils(const E *row, int dim, bool seen) {
+  typedef vec<unsigned short, 8> bits;
+  const bits inf = (unsigned short)(is_half<E> ? 0x7c00 : 0x7f80);
+  bits most = 0, off = 0x7fff;  // largest magnitude; how near one comes to an infinity
+#pragma unroll 1
+  for (int d = 0; d < dim; d += 32) {  // the loads of 32 elements together
+    bits x[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) x[k] = *(const bits *)(row + (d + 8 * k < dim ? d + 8 * k : 0));
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      x[k] &= (unsigned short)0x7fff;
+      most = __builtin_elementwise_max(most, x[k]);
+      off = __builtin_elementwise_min(off, x[k] ^ inf);
+    }
+  }
+  int top = 0, near = 0x7fff;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    top = max(top, (int)most[i]);
+    near = min(near, (int)off[i]);
+  }
+  return near == 0 || (!seen && top > inf[0]);
+}
+
+// What n <= 64 queries from t0 on see: the first key and the end of all their spans, then
+// those of the keys that all of them see.
+__device__ __forceinline__ int4 rows_see(const AttnK &p, int b, int t0, int n, int lane) {
+  const bool on = lane < n;
+  const int2 s = on ? row_span(p, b, t0 + lane) : make_int2(0, 0);
+  return {wave_min(s.x < s.y ? s.x : INT32_MAX), wave_max(s.y), wave_max(on ? s.x : 0),
+          wave_min(on ? s.y : INT32_MAX)};
+}
+
+// Whether x (keys or values) holds a row that spoils among those of the tiles of T rows
+// that queries were multiplied with and that not all of them see (`see` of rows_see); with
+// SEEN also among those that all see.
+template <class E, int T, bool SEEN>
+__device__ __forceinline__ bool keys_spoil(const AttnK &p, const TokK &x, int b, int kvh, int4 see,
+                                           int lane) {
+  if (see.x >= see.y) return false;
+  const int end = min((see.y + T - 1) / T * T, p.kv_len);
+#pragma unroll 1
+  for (int j0 = see.x / T * T; j0 < end; j0 += 64) {
+    const int j = j0 + lane;
+    const bool seen = j >= see.z && j < see.w;
+    bool bad = false;
+    if (j < end && (SEEN || !seen)) bad = row_spoils(tok_row<E>(x, b, j, kvh), p.dim, seen);
+    if (__builtin_amdgcn_ballot_w64(bad)) return true;
+  }
+  return false;
+}
+
+// A sum of rows that a wave does again: 16 lanes a row, eight elements in each, four rows
+// (j % 4 = lane / 16) at a time.
+struct RowSum {
+  float a[8] = {};
+
+  // += w_j x_j of the rows j0 + j with bit j of `some` (j < 64; w of lane j), none of them
+  // past `last`. Returns whether anything is not NaN yet.
+  template <class E>
+  __device__ __forceinline__ bool add(float w, uint64_t some, const TokK &x, int b, int head,
+                                      int j0, int last, int dim, int lane) {
+    const int e = 8 * (lane & 15), group = lane >> 4;
+    bool open = true;
+#pragma unroll 1
+    for (int j1 = 0; open && j1 < 64 && some >> j1; j1 += 16) {
+      frag<E> f[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        f[i] = *(const frag<E> *)(tok_row<E>(x, b, min(j0 + j1 + 4 * i + group, last), head) +
+                                  (e < dim ? e : 0));
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int j = j1 + 4 * i + group;
+        const float wj = __shfl(w, j);
+        const bool on = some >> j & 1;
+#pragma unroll
+        for (int c = 0; c < 8; c++) a[c] = on ? fmaf(wj, (float)f[i][c], a[c]) : a[c];
+      }
+      float left = a[0];  // NaN where all are
+#pragma unroll
+      for (int c = 1; c < 8; c++) left = fmaxf(left, a[c]);
+      open = __builtin_amdgcn_ballot_w64(e < dim && left == left);
+    }
+    return open;
+  }
+
+  __device__ __forceinline__ void shrink(float by) {
+#pragma unroll
+    for (int c = 0; c < 8; c++) a[c] *= by;
+  }
+
+  // The sum times `by`, stored.
+  template <class E>
+  __device__ __forceinline__ void store(E *row, float by, int dim, int lane) {
+    frag<E> f;
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+      a[c] += __shfl_xor(a[c], 16);
+      a[c] += __shfl_xor(a[c], 32);
+      f[c] = (E)(a[c] * by);
+    }
+    if (lane < 16 && 8 * lane < dim) *(frag<E> *)(row + 8 * lane) = f;
+  }
+};
+
+__device__ __forceinline__ uint64_t first_bits(int n) { return n < 64 ? (1ull << n) - 1 : ~0ull; }
+
+// (32 elements at a time, their loads together)
 template <class E>
 __device__ __forceinline__ float dot_row(const E *a, const E *b, int dim) {
   float s = 0.0f;
-  for (int d = 0; d < dim; d += 8) {
-    const vec<E, 8> x = *(const vec<E, 8> *)(a + d), y = *(const vec<E, 8> *)(b + d);
+#pragma unroll 1
+  for (int d = 0; d < dim; d += 32) {
+    frag<E> x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) s = fmaf((float)x[i], (float)y[i], s);
+    for (int k = 0; k < 4; k++) {
+      const int at = d + 8 * k < dim ? d + 8 * k : 0;
+      x[k] = *(const frag<E> *)(a + at);
+      y[k] = *(const frag<E> *)(b + at);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      if (d + 8 * k >= dim) continue;
+#pragma unroll
+      for (int i = 0; i < 8; i++) s = fmaf((float)x[k][i], (float)y[k][i], s);
+    }
   }
   return s;
 }

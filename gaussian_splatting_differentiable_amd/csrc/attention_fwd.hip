@@ -21,17 +21,17 @@
 namespace {
 
 // ------------------------------------------------------------ rows done again
-// 0 x NaN and 0 x infinity are NaN: in a matrix product, a masked key whose value
-// row is not finite spoils rows that do not see it. A row whose result holds a
-// NaN is therefore computed again from its own keys alone, by one wave: a lane
-// takes a key's score, then two elements of the output.
+// One row's o (its lse is right: masked scores are replaced): a lane takes a key's score.
 template <class E>
-__device__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
+__device__ __forceinline__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
   const int2 span = row_span(p, b, t);
   const int kvh = head / p.share;
   const E *q = tok_row<E>(p.q, b, t, head);
-  float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-  for (int j0 = span.x; j0 < span.y; j0 += 64) {
+  float m = -INFINITY, l = 0.0f;
+  RowSum o;
+  bool open = true;
+#pragma unroll 1
+  for (int j0 = span.x; open && j0 < span.y; j0 += 64) {
     const int n = min(64, span.y - j0);
     float s = -INFINITY;
     if (lane < n) s = dot_row(q, tok_row<E>(p.k, b, j0 + lane, kvh), p.dim) * p.scale_log2;
@@ -39,23 +39,11 @@ __device__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
     const float w = lane < n ? __builtin_amdgcn_exp2f(s - ref) : 0.0f;
     const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
     l = l * shrink + group_sum(w, 64);
-    o0 *= shrink;
-    o1 *= shrink;
+    o.shrink(shrink);
     m = top;
-    for (int j = 0; j < n; j++) {
-      const E *v = tok_row<E>(p.v, b, j0 + j, kvh);
-      const float wj = __shfl(w, j);
-      if (lane < p.dim) o0 = fmaf(wj, (float)v[lane], o0);
-      if (lane + 64 < p.dim) o1 = fmaf(wj, (float)v[lane + 64], o1);
-    }
+    open = o.add<E>(w, first_bits(n), p.v, b, kvh, j0, span.y - 1, p.dim, lane);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  E *o = tok_row<E>(p.o, b, t, head);
-  if (lane < p.dim) o[lane] = (E)(o0 * inv);
-  if (lane + 64 < p.dim) o[lane + 64] = (E)(o1 * inv);
-  if (lane == 0)
-    p.lse[((int64_t)b * p.q_heads + head) * p.q_len + t] =
-        l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
+  o.store(tok_row<E>(p.o, b, t, head), l == 0.0f ? 0.0f : 1.0f / l, p.dim, lane);
 }
 
 // How far the reference is below the largest score when it moves, and how far a score may
@@ -272,9 +260,7 @@ __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int 
       sm.o[d][i] *= inv;
       nan |= sm.o[d][i] != sm.o[d][i];
     }
-  uint64_t again = __builtin_amdgcn_ballot_w64(on && nan);
-  again = (again | again >> 32) & 0xffffffffu;
-  if (on && !(again >> (lane & 31) & 1)) {
+  if (on) {
     E *o = tok_row<E>(p.o, b, t, head);
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
@@ -289,10 +275,18 @@ __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int 
           l == 0.0f ? -INFINITY
                     : ((sm.m == -INFINITY ? 0.0f : sm.m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
   }
+  // (with a sum that is NaN all of o is)
+  uint64_t again = __builtin_amdgcn_ballot_w64(on && nan && l == l);
+  again = (again | again >> 32) & 0xffffffffu;
+  if (!again) return;
+  const AttnK &c = args_again();
+  const int4 see = {lo, hi, in_lo, in_hi};
+  if (!keys_spoil<E, KT, is_half<E>>(c, c.v, b, kvh, see, lane)) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the stores above come first
   while (again) {
     const int r = __builtin_ctzll(again);
     again &= again - 1;
-    redo_row<E>(p, b, head, tile0 + wave * 32 + r, lane);
+    redo_row<E>(c, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
@@ -440,13 +434,17 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   if (live && (tid & 7) == 0)
     p.lse[at_row] = l == 0.0f ? -INFINITY
                               : ((m == -INFINITY ? 0.0f : m) + __builtin_amdgcn_logf(l)) * ATTN_LN2;
-  // Rows of this wave whose result holds a NaN, after its stores.
-  uint64_t again = __builtin_amdgcn_ballot_w64(nan);
-  if (again) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  // Rows of this wave, as above.
+  uint64_t again = __builtin_amdgcn_ballot_w64(nan && l == l);
+  if (!again) return;
+  const AttnK &c = args_again();
+  const int4 see = {lo, hi, in_lo, in_hi};
+  if (!keys_spoil<E, FT, is_half<E>>(c, c.v, b, kvh, see, lane)) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
   for (int k = 0; k < 8 && again; k++) {
     if (!(again >> (8 * k) & 0xff)) continue;
     const unsigned r3 = rt * 32u + wave * 8 + k;
-    redo_row<E>(p, b, kvh * p.share + (int)(r3 % share), (int)(r3 / share), lane);
+    redo_row<E>(c, b, kvh * c.share + (int)(r3 % share), (int)(r3 / share), lane);
   }
 }
 
@@ -510,16 +508,20 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
   const unsigned bh = (unsigned)row / (unsigned)p.q_len;  // (row is below 2^29)
   const int t = (int)((unsigned)row - bh * p.q_len), b = (int)(bh / (unsigned)p.q_heads);
   const int head = (int)(bh - (unsigned)b * p.q_heads);
-  if (__builtin_amdgcn_ballot_w64(o0 != o0 || o1 != o1)) {
-    redo_row<E>(p, b, head, t, lane);
-    return;
-  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   E *to = tok_row<E>(p.o, b, t, head);
   if (lane < p.dim) to[lane] = (E)(o0 * inv);
   if (lane + 64 < p.dim) to[lane + 64] = (E)(o1 * inv);
   if (lane == 0)
     p.lse[row] = l == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * ATTN_LN2;
+  if (l != l || !__builtin_amdgcn_ballot_w64(o0 != o0 || o1 != o1)) return;
+  // the tokens of this row's block of 32
+  const AttnK &c = args_again();
+  const int share = c.share, kvh = head / share, r0 = (t * share + head - kvh * share) / 32 * 32;
+  const int t0 = r0 / share, n = min((r0 + 31) / share, c.q_len - 1) - t0 + 1;
+  if (!keys_spoil<E, FT, is_half<E>>(c, c.v, b, kvh, rows_see(c, b, t0, n, lane), lane)) return;
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  redo_row<E>(c, b, head, t, lane);
 }
 
 template <class E, int D>

@@ -125,3 +125,105 @@ def test_small_probabilities_of_a_long_row_in_fp16(nq, H):
     want, room = small / (1 + small), n * 2.0 ** -30 + 4 * 2.0 ** -11 * small
     assert float((o.double() - want).abs().max()) <= room
     assert float((lse.double() - (18.0 + math.log1p(small))).abs().max()) <= 1e-5 * 18
+
+
+# ------------------------------------------------- a NaN that is seen
+
+def _time(call):
+    call()
+    best = math.inf
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("mask", ["none", "causal", "packed"])
+@pytest.mark.parametrize("where", ["value", "values", "all"])
+def test_a_nan_that_is_seen_does_not_slow_a_call_down(mask, where):
+    """A diverged step's NaN is there at the cost of a call, ten times at most, not that of every
+    pair by itself: nothing masked has spoilt those rows, or they are NaN from the first key on."""
+    tok = _tokens()
+    q, k, v, do = _inputs(5, 1, 2048, 2048, 8, 8, 64, BF)
+    how = dict(causal=mask == "causal",
+               spans=_list((1000, 0, 1000), (1048, 1000, 2048)) if mask == "packed" else None)
+
+    def step():
+        o, lse = tok.attention(q, k, v, **how)
+        return o, tok.attention_bwd(do, q, k, v, o, lse, **how)
+
+    base = _time(step)
+    if where == "value":
+        v[:, 5] = math.nan
+    elif where == "values":
+        v.fill_(math.nan)
+    else:
+        for t in (q, k, v, do):
+            t.fill_(math.nan)
+    took = _time(step)
+    o, (dq, dk, dv) = step()
+    rows = torch.ones(2048, dtype=torch.bool, device="cuda")
+    if where == "value":
+        rows[:5] = mask != "causal"
+        rows[1000:] = mask != "packed"
+    for t in (o, dq):
+        assert torch.equal(torch.isnan(t).all(3).all(2)[0], rows), mask
+        assert torch.equal(torch.isnan(t).any(3).any(2)[0], rows), mask
+    assert took <= 10 * base, (took, base)
+
+
+@pytest.mark.parametrize("mask", ["none", "packed"])
+@pytest.mark.parametrize("H,n", [(2, 300), (64, 300)])
+def test_an_infinity_that_is_seen_with_the_smallest_probabilities(mask, H, n):
+    """p v with p of about 2^-50, which is 0 in fp16, and an infinite v is infinite, not NaN; and
+    so is p do in dv."""
+    tok = _tokens()
+    q, k, v, do = _inputs(15, 1, n, n, H, H, 64, FP)
+    q[..., 0], k[..., 0] = 4.0, 0.0
+    k[:, 20, :, 0] = -70.0  # a score of -35 beside those of the others
+    v[:, 20, :, 7] = math.inf
+    how = dict(spans=_list((n - 130, 0, n - 130), (130, n - 130, n)) if mask == "packed" else None)
+    sees = n - 130 if mask == "packed" else n
+    o, lse = tok.attention(q, k, v, **how)
+    assert torch.all(o[:, :sees, :, 7] == math.inf) and torch.isfinite(o[:, sees:]).all()
+    assert int((~torch.isfinite(o)).sum()) == sees * H
+    v[:, 20, :, 7] = 0.5
+    do[:, 30, :, 9] = math.inf
+    o, lse = tok.attention(q, k, v, **how)
+    _, _, dv = tok.attention_bwd(do, q, k, v, o, lse, **how)
+    assert torch.all(dv[:, :sees, :, 9] == math.inf) and torch.isfinite(dv[:, sees:]).all()
+    assert int((~torch.isfinite(dv)).sum()) == sees * H
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,nq,nk", [(2, 3, 9000), (6, 700, 700), (64, 150, 150)])
+def test_a_masked_nan_beside_a_nan_that_is_seen(H, nq, nk, dtype):
+    """Rows whose own NaN is in one element, in tiles where a masked key holds a NaN too, in the
+    form for few rows (whole and in parts) and in that for many."""
+    tok = _tokens()
+    q, k, v, do = _inputs(16, 1, nq, nk, H, H // 2, 64, dtype)
+    cut = nk - 100
+    spans = _list((nq - 1, 0, cut), (1, cut, nk))  # the last query sees the last keys alone
+    v[:, cut - 3, :, 5], v[:, cut + 2, :, 6] = math.nan, math.nan
+    do[:, nq - 1, :, 8] = math.nan
+    o, lse = tok.attention(q, k, v, spans=spans)
+    bad = torch.zeros(1, nq, H, 64, dtype=torch.bool, device="cuda")
+    bad[:, :nq - 1, :, 5], bad[:, nq - 1, :, 6] = True, True
+    assert torch.equal(torch.isnan(o), bad)
+    allowed = ref.spans_of(nq, nk, spans)
+    clean = v.clone()
+    clean[:, cut - 3, :, 5], clean[:, cut + 2, :, 6] = 0.0, 0.0
+    want = ref.attention(q, k, clean, allowed, 0.125)
+    ref.check("o", torch.where(bad, torch.zeros_like(o), o),
+              (torch.where(bad.cpu(), 0.0, want["o"][0]), want["o"][1]))
+    ref.check("lse", lse, want["lse"])
+    # the gradients' NaN: a row's D is NaN with its o, so dq is, and dk of all that it sees
+    dq, dk, dv = tok.attention_bwd(do, q, k, v, o, lse, spans=spans)
+    assert torch.isnan(dq).all() and torch.isnan(dk).all()
+    sees = torch.zeros(1, nk, H // 2, 64, dtype=torch.bool, device="cuda")
+    sees[:, cut:, :, 8] = True
+    assert torch.equal(torch.isnan(dv), sees)
