@@ -1,5 +1,5 @@
-"""The token operators where results must not depend on what they do not see and at the ends of
-their ranges, against the formulas in 64 bits."""
+"""The token operators where results must not depend on what they do not see, at the ends of
+their ranges, and on the paths that only large calls take, against the formulas in 64 bits."""
 import math
 
 import pytest
@@ -227,3 +227,74 @@ def test_a_masked_nan_beside_a_nan_that_is_seen(H, nq, nk, dtype):
     sees = torch.zeros(1, nk, H // 2, 64, dtype=torch.bool, device="cuda")
     sees[:, cut:, :, 8] = True
     assert torch.equal(torch.isnan(dv), sees)
+
+
+# ------------------------------------------------- the ends of the ranges
+
+@pytest.mark.parametrize("scale,by_q,by_k", [(2.0 ** -100, 2.0 ** 49, 2.0 ** 48),
+                                             (2.0 ** 100, 2.0 ** -53, 2.0 ** -50)])
+def test_scales_at_the_ends(scale, by_q, by_k):
+    q, k, v, do = _inputs(6, 1, 150, 170, 2, 1, 64, BF)
+    _compare(q * by_q, k * by_k, v, do, scale=scale)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, FP)])
+def test_spans_with_so_many_blocks_that_one_pass_takes_both_sequences(d, dtype):
+    """4096 blocks of rows: a block walks over the keys of both sequences that it has rows of."""
+    B, H, n = 16, 128, 140
+    q, k, v, do = _inputs(7, B, n, n, H, H, d, dtype)
+    spans = _list((60, 0, 60), (50, 60, 110), (20, 105, 140), (10, 0, 0))
+    got = _run(q, k, v, do, spans=spans)
+    allowed = ref.spans_of(n, n, spans)
+    for b, h in ((0, 0), (0, 127), (7, 61), (15, 3), (15, 127)):
+        cut = [t[b:b + 1, :, h:h + 1] for t in (q, k, v, do)]
+        want = ref.attention(*cut[:3], allowed, 1 / math.sqrt(d), cut[3])
+        for name, x in got.items():
+            ref.check(name, x[b:b + 1, h:h + 1] if name == "lse" else x[b:b + 1, :, h:h + 1],
+                      want[name])
+
+
+@pytest.mark.parametrize("mask", ["none", "late", "ends"])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (64, FP), (128, BF)])
+def test_more_queries_than_a_block_of_keys_lists_at_a_time(mask, d, dtype):
+    """2^18 + 70 queries of 40 keys: the keys' blocks walk twice over the tiles of queries. With
+    all of them, with those of the second walk alone, and with a few of each."""
+    n, nk = (1 << 18) + 70, 40
+    q, k, v, do = _inputs(8, 1, n, nk, 1, 1, d, dtype)
+    spans = {"none": None, "late": _list((1 << 18, 0, 0), (70, 0, nk)),
+             "ends": _list((100, 3, nk), ((1 << 18) - 50, 0, 0), (20, 0, 17))}[mask]
+    _compare(q, k, v, do, spans=spans)
+
+
+# ------------------------------------------------- streams and autograd
+
+def test_norm_and_rotation_on_another_stream_into_given_outputs():
+    tok = _tokens()
+    q, k = _randn(9, 2, 100, 4, 64), _randn(10, 2, 100, 2, 64)
+    w = torch.rand(64).cuda() + 0.5
+    want = tok.qk_norm_rope(q, k, w, w)
+    grads = tok.qk_norm_rope_bwd(*want, q, k, w, w)
+    s, outs = torch.cuda.Stream(), (torch.empty_like(q), torch.empty_like(k))
+    s.wait_stream(torch.cuda.current_stream())
+    got = tok.qk_norm_rope(q, k, w, w, q_out=outs[0], k_out=outs[1], stream=s)
+    back = tok.qk_norm_rope_bwd(*got, q, k, w, w, stream=s)
+    s.synchronize()
+    assert got[0] is outs[0] and got[1] is outs[1]
+    for a, b in zip((*got, *back), (*want, *grads)):
+        assert torch.equal(a, b)
+
+
+def test_autograd_of_queries_alone_and_of_dropped_rows():
+    tok = _tokens()
+    q, w = _randn(11, 1, 9, 4, 64), torch.rand(64).cuda() + 0.5
+    xs = [t.clone().requires_grad_() for t in (q, w)]
+    y, none = tok.QkNormRope.apply(xs[0], None, xs[1], None, None, None, False, 1e-6)
+    assert none is None
+    y.backward(torch.ones_like(y))
+    dq, _, dw, _ = tok.qk_norm_rope_bwd(torch.ones_like(q), None, q, None, w, None)
+    assert torch.equal(xs[0].grad, dq) and torch.equal(xs[1].grad, dw)
+    x, r, g = (_randn(i, 20, 30) for i in (12, 13, 14))
+    xs = [t.clone().requires_grad_() for t in (x, r)]
+    tok.Dropout.apply(*xs, 0.4, 6, 7, True).backward(g)
+    assert torch.equal(xs[0].grad, tok.dropout(g, 0.4, 6, 7, per_row=True))
+    assert torch.equal(xs[1].grad, g)
