@@ -39,35 +39,35 @@ __device__ __forceinline__ int too_many(float top) {
 
 // ------------------------------------------------------------ rows done again
 
-template <class E>
+template <class E, int N>
 __device__ __forceinline__ void redo_query(const AttnK &p, int b, int head, int t, int lane) {
   const int2 span = row_span(p, b, t);
   const int kvh = head / p.share;
   const int64_t bh = (int64_t)b * p.q_heads + head;
   const E *q = tok_row<E>(p.q, b, t, head), *g = tok_row<E>(p.d_o, b, t, head);
   const float lse = p.lse[bh * p.q_len + t] * ATTN_LOG2E, delta = -p.row_delta[bh * p.q_pad + t];
-  RowSum dq;
+  RowSum<N> dq;
   bool open = true;
 #pragma unroll 1
   for (int j0 = span.x; open && j0 < span.y; j0 += 64) {
     const int n = min(64, span.y - j0);
     float ds = 0.0f;
     if (lane < n) {
-      const float s = dot_row(q, tok_row<E>(p.k, b, j0 + lane, kvh), p.dim) * p.scale_log2;
+      const float s = dot_row<4>(q, tok_row<E>(p.k, b, j0 + lane, kvh), p.dim) * p.scale_log2;
       ds = __builtin_amdgcn_exp2f(s - lse) *
-           (dot_row(g, tok_row<E>(p.v, b, j0 + lane, kvh), p.dim) - delta);
+           (dot_row<4>(g, tok_row<E>(p.v, b, j0 + lane, kvh), p.dim) - delta);
     }
-    open = dq.add<E>(ds, first_bits(n), p.k, b, kvh, j0, span.y - 1, p.dim, lane);
+    open = dq.template add<E>(ds, first_bits(n), p.k, b, kvh, j0, span.y - 1, p.dim, lane);
   }
   dq.store(tok_row<E>(p.dq, b, t, head), p.scale, p.dim, lane);
 }
 
 // One key's row of dV, or of dK.
-template <class E>
+template <class E, int N>
 __device__ __forceinline__ void redo_key(const AttnK &p, int b, int kvh, int key, bool of_v, int lane) {
   const E *k = tok_row<E>(p.k, b, key, kvh), *v = tok_row<E>(p.v, b, key, kvh);
   const TokK x = of_v ? p.d_o : p.q;
-  RowSum sum;
+  RowSum<N> sum;
   bool open = true;
 #pragma unroll 1
   for (int head = kvh * p.share; head < (kvh + 1) * p.share; head++)
@@ -81,12 +81,12 @@ __device__ __forceinline__ void redo_key(const AttnK &p, int b, int kvh, int key
       float w = 0.0f;
       if (in) {
         const int64_t bh = (int64_t)b * p.q_heads + head;
-        const float s = dot_row(tok_row<E>(p.q, b, t, head), k, p.dim) * p.scale_log2;
+        const float s = dot_row<4>(tok_row<E>(p.q, b, t, head), k, p.dim) * p.scale_log2;
         w = __builtin_amdgcn_exp2f(s - p.lse[bh * p.q_len + t] * ATTN_LOG2E);
         if (!of_v)
-          w *= dot_row(tok_row<E>(p.d_o, b, t, head), v, p.dim) + p.row_delta[bh * p.q_pad + t];
+          w *= dot_row<4>(tok_row<E>(p.d_o, b, t, head), v, p.dim) + p.row_delta[bh * p.q_pad + t];
       }
-      open = sum.add<E>(w, seen, x, b, head, t0, p.q_len - 1, p.dim, lane);
+      open = sum.template add<E>(w, seen, x, b, head, t0, p.q_len - 1, p.dim, lane);
     }
   sum.store(tok_row<E>(of_v ? p.dv : p.dk, b, key, kvh), of_v ? 1.0f : p.scale, p.dim, lane);
 }
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
   while (again) {
     const int r = __builtin_ctz(again);
     again &= again - 1;
-    redo_key<E>(c, b, kvh, mine0 + r, half, lane);
+    redo_key<E, 8>(c, b, kvh, mine0 + r, half, lane);
   }
 }
 
@@ -700,7 +700,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles) {
   while (again) {
     const int r = __builtin_ctz(again);
     again &= again - 1;
-    redo_query<E>(c, b, head, tile0 + wave * 32 + r, lane);
+    redo_query<E, 8>(c, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
@@ -739,10 +739,14 @@ __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
     store4(tok_row<E>(KEYS ? p.dk : p.dq, b, t, head) + e, x);
     if (KEYS) store4(tok_row<E>(p.dv, b, t, head) + e, y);
   }
-  bool nan = false;
+  bool x_nan = false, y_nan = false;
 #pragma unroll
-  for (int i = 0; i < 4; i++) nan |= x[i] != x[i] || y[i] != y[i];
-  const uint64_t bits = __builtin_amdgcn_ballot_w64(nan);
+  for (int i = 0; i < 4; i++) {
+    x_nan |= x[i] != x[i];
+    y_nan |= y[i] != y[i];
+  }
+  const uint64_t x_bits = __builtin_amdgcn_ballot_w64(x_nan), y_bits = __builtin_amdgcn_ballot_w64(y_nan);
+  const uint64_t bits = x_bits | y_bits;
   if (!bits) return;
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the stores above come first
   const AttnK &c = args_again();
@@ -758,21 +762,22 @@ __device__ __forceinline__ void sum_rows(const AttnK &p, int block) {
       const int n = min(min((64 - i) / LANES, first + most - ht), (KEYS ? c.kv_len : c.q_len) - ht);
       until = i + n * LANES;
       if (KEYS) {
-        spoilt[0] = queries_spoil<E>(c, hb, hh, first, ht, n, false, lane);
-        spoilt[1] = queries_spoil<E>(c, hb, hh, first, ht, n, true, lane);
+        spoilt[0] = x_bits && queries_spoil<E>(c, hb, hh, first, ht, n, false, lane);
+        spoilt[1] = y_bits && queries_spoil<E>(c, hb, hh, first, ht, n, true, lane);
       } else {
         const int4 s = rows_see(c, hb, first, min(most, c.q_len - first), lane);
         spoilt[0] = keys_spoil<E, KT, false>(c, c.k, hb, hh / c.share, s, lane);
       }
     }
     if (KEYS) {
-      if (spoilt[0]) redo_key<E>(c, hb, hh, ht, false, lane);
-      if (spoilt[1]) redo_key<E>(c, hb, hh, ht, true, lane);
+      const uint64_t row = ((1ull << LANES) - 1) << i;
+      if (spoilt[0] && x_bits & row) redo_key<E, 4>(c, hb, hh, ht, false, lane);
+      if (spoilt[1] && y_bits & row) redo_key<E, 4>(c, hb, hh, ht, true, lane);
     } else if (spoilt[0]) {
       const int64_t bh = (int64_t)hb * c.q_heads + hh;
       const float lse = c.lse[bh * c.q_len + ht], delta = c.row_delta[bh * c.q_pad + ht];
       const int2 s = row_span(c, hb, ht);
-      if (s.x >= s.y || (lse == lse && delta == delta)) redo_query<E>(c, hb, hh, ht, lane);
+      if (s.x >= s.y || (lse == lse && delta == delta)) redo_query<E, 4>(c, hb, hh, ht, lane);
     }
   }
 }

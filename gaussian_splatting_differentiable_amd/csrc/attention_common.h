@@ -351,7 +351,9 @@ __device__ __forceinline__ bool keys_spoil(const AttnK &p, const TokK &x, int b,
 }
 
 // A sum of rows that a wave does again: 16 lanes a row, eight elements in each, four rows
-// (j % 4 = lane / 16) at a time.
+// (j % 4 = lane / 16) at a time, the loads of 4 N rows together (N: as the kernel has
+// registers).
+template <int N>
 struct RowSum {
   float a[8] = {};
 
@@ -363,14 +365,14 @@ struct RowSum {
     const int e = 8 * (lane & 15), group = lane >> 4;
     bool open = true;
 #pragma unroll 1
-    for (int j1 = 0; open && j1 < 64 && some >> j1; j1 += 16) {
-      frag<E> f[4];
+    for (int j1 = 0; open && j1 < 64 && some >> j1; j1 += 4 * N) {
+      frag<E> f[N];
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < N; i++)
         f[i] = *(const frag<E> *)(tok_row<E>(x, b, min(j0 + j1 + 4 * i + group, last), head) +
                                   (e < dim ? e : 0));
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
+      for (int i = 0; i < N; i++) {
         const int j = j1 + 4 * i + group;
         const float wj = __shfl(w, j);
         const bool on = some >> j & 1;
@@ -406,21 +408,21 @@ struct RowSum {
 
 __device__ __forceinline__ uint64_t first_bits(int n) { return n < 64 ? (1ull << n) - 1 : ~0ull; }
 
-// (32 elements at a time, their loads together)
-template <class E>
+// (the loads of 8 N elements together)
+template <int N, class E>
 __device__ __forceinline__ float dot_row(const E *a, const E *b, int dim) {
   float s = 0.0f;
 #pragma unroll 1
-  for (int d = 0; d < dim; d += 32) {
-    frag<E> x[4], y[4];
+  for (int d = 0; d < dim; d += 8 * N) {
+    frag<E> x[N], y[N];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
+    for (int k = 0; k < N; k++) {
       const int at = d + 8 * k < dim ? d + 8 * k : 0;
       x[k] = *(const frag<E> *)(a + at);
       y[k] = *(const frag<E> *)(b + at);
     }
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
+    for (int k = 0; k < N; k++) {
       if (d + 8 * k >= dim) continue;
 #pragma unroll
       for (int i = 0; i < 8; i++) s = fmaf((float)x[k][i], (float)y[k][i], s);

@@ -22,26 +22,26 @@ namespace {
 
 // ------------------------------------------------------------ rows done again
 // One row's o (its lse is right: masked scores are replaced): a lane takes a key's score.
-template <class E>
+template <class E, int N>
 __device__ __forceinline__ void redo_row(const AttnK &p, int b, int head, int t, int lane) {
   const int2 span = row_span(p, b, t);
   const int kvh = head / p.share;
   const E *q = tok_row<E>(p.q, b, t, head);
   float m = -INFINITY, l = 0.0f;
-  RowSum o;
+  RowSum<N> o;
   bool open = true;
 #pragma unroll 1
   for (int j0 = span.x; open && j0 < span.y; j0 += 64) {
     const int n = min(64, span.y - j0);
     float s = -INFINITY;
-    if (lane < n) s = dot_row(q, tok_row<E>(p.k, b, j0 + lane, kvh), p.dim) * p.scale_log2;
+    if (lane < n) s = dot_row<4>(q, tok_row<E>(p.k, b, j0 + lane, kvh), p.dim) * p.scale_log2;
     const float top = fmaxf(m, wave_fmax(s)), ref = top == -INFINITY ? 0.0f : top;
     const float w = lane < n ? __builtin_amdgcn_exp2f(s - ref) : 0.0f;
     const float shrink = __builtin_amdgcn_exp2f((m == -INFINITY ? ref : m) - ref);
     l = l * shrink + group_sum(w, 64);
     o.shrink(shrink);
     m = top;
-    open = o.add<E>(w, first_bits(n), p.v, b, kvh, j0, span.y - 1, p.dim, lane);
+    open = o.template add<E>(w, first_bits(n), p.v, b, kvh, j0, span.y - 1, p.dim, lane);
   }
   o.store(tok_row<E>(p.o, b, t, head), l == 0.0f ? 0.0f : 1.0f / l, p.dim, lane);
 }
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int 
   while (again) {
     const int r = __builtin_ctzll(again);
     again &= again - 1;
-    redo_row<E>(c, b, head, tile0 + wave * 32 + r, lane);
+    redo_row<E, 8>(c, b, head, tile0 + wave * 32 + r, lane);
   }
 }
 
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_few(AttnK p, int row_tiles) {
   for (int k = 0; k < 8 && again; k++) {
     if (!(again >> (8 * k) & 0xff)) continue;
     const unsigned r3 = rt * 32u + wave * 8 + k;
-    redo_row<E>(c, b, kvh * c.share + (int)(r3 % share), (int)(r3 / share), lane);
+    redo_row<E, 8>(c, b, kvh * c.share + (int)(r3 % share), (int)(r3 / share), lane);
   }
 }
 
@@ -521,7 +521,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnK p) {
   const int t0 = r0 / share, n = min((r0 + 31) / share, c.q_len - 1) - t0 + 1;
   if (!keys_spoil<E, FT, is_half<E>>(c, c.v, b, kvh, rows_see(c, b, t0, n, lane), lane)) return;
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  redo_row<E>(c, b, head, t, lane);
+  redo_row<E, 4>(c, b, head, t, lane);
 }
 
 template <class E, int D>
