@@ -11,8 +11,9 @@
 // by atomics, so results do not depend on timing, and nothing of size q_len x kv_len
 // is ever stored.
 //
-// p and ds are rounded to the inputs' 16-bit type for the products, which makes dq's and
-// dk's error 1.45 to 1.6 times that of rounding the results alone. Probabilities
+// p and ds are rounded to the inputs' 16-bit type for the products: against 64 bits dv's
+// error is 1.3 to 1.43 times that of rounding the results alone, dq's and dk's 1.4 to 1.55,
+// and up to 1.67 where rows see a few dozen keys (D, below). Probabilities
 // of long rows fall below the normal range of fp16 (2^-14), so for fp16 the
 // kernels work on p 2^15 and on ds 2^e, powers of two that are taken out of the 32-bit
 // sums. e is each key's own in dK and each query's in dQ, and falls as the largest |ds| of
@@ -260,8 +261,8 @@ __device__ __forceinline__ void store_part(const f32x16 (&acc)[D / 32], float by
 // few such blocks, or masks make them uneven, a block takes one of kv_parts equal runs
 // of those tiles, and k_attn_sum adds the parts' 32-bit sums. -lse / scale and -D_i are
 // the accumulators' starting values. Bound by the matrix units: 16384 tokens, 8 heads of
-// 128 on 2, bf16: 1990 us, 1105 TFLOP/s of its four products (four waves a block, 32
-// keys each and all rows: 2350 us).
+// 128 on 2, bf16: 1930 us, 1140 TFLOP/s of its four products (four waves a block, 32
+// keys each and all rows, took 18% longer).
 template <class E, int D>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int q_tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then
@@ -546,7 +547,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_kv(AttnK p, int tiles, int 
 // The forward's walk with a second score product and without a running maximum; a
 // block takes one of q_parts runs of its key tiles, as above. Bound by the matrix
 // units' rate at the clock that their power leaves: 16384 tokens, 8 heads of 128, bf16:
-// 1370 us, 1200 TFLOP/s of its three products. Heads of 65 to 96 have a form of 96 (2 x 2048 queries,
+// 1350 us, 1220 TFLOP/s of its three products. Heads of 65 to 96 have a form of 96 (2 x 2048 queries,
 // 12 heads of 80, bf16: 74 us, in the form of 128 90).
 template <class E, int D>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnK p, int tiles) {
@@ -826,7 +827,9 @@ hipError_t launch(const AttnK &p, hipStream_t st) {
 // compute units, every part with four tiles or more. With spans at least two where the
 // blocks are no more than one for each; with causal rows, whose blocks are the most
 // uneven, as many as make two for each, of six tiles or more. A part costs the write and
-// the read of its 32-bit sums.
+// the read of its 32-bit sums. No more than 16, which keeps the workspace to 16 results in 32
+// bits; few queries over many keys would gain by more (16384 keys, 8 heads of 128, 1 query:
+// 93 us, with up to 32 parts 87; 262144 keys, 2 heads, 64 queries: 660 and 497).
 // Measured, q_len 2331, 8 heads of 64 with spans (152 blocks): dK and dV in one part 55
 // us, in two 38 and their sum 7, in four 49 and 8; dQ in one part 35, in two 24 and their
 // sum 5. Causal, whole backward, 4096 tokens, 16 heads of 128 on 4 (128 blocks of keys):

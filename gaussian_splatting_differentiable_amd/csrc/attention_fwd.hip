@@ -11,9 +11,9 @@
 // largest at most.
 // With many rows a wave looks for its largest scores in the first tile only. Later
 // tiles compute p with the reference that is there; if a lane's sum of them passes 2^13
-// (fp16: 2^15; or is NaN), the wave computes the tile's scores again and looks. Measured, 2 x 8192
-// tokens, 16 heads of 64: 670 us, looking at every tile 705; with few rows (2331 tokens,
-// 8 heads of 64) 27 us and 24, there every tile is looked at.
+// (fp16: 2^15; or is NaN), the wave computes the tile's scores again and looks. Both measured
+// in turn: 2 x 8192 tokens, 16 heads of 64: 5% less than looking at every tile; with few rows
+// (2331 tokens, 8 heads of 64) 27 us and 24, there every tile is looked at.
 // p is rounded to the inputs' 16-bit type for the second product, as matrix
 // instructions take it; l sums the unrounded p.
 #include "attention_common.h"
@@ -173,11 +173,12 @@ struct Softmax {
 // of their spans through LDS in tiles of 64, the next one on its way while this one is
 // computed.
 // Bound by the matrix units, and in short calls by how evenly blocks fall on the
-// compute units: 16384 tokens, 8 heads of 128, bf16: 1010 us, 1090 TFLOP/s. Heads of 65
+// compute units: 16384 tokens, 8 heads of 128, bf16: 985 us, 1116 TFLOP/s. Heads of 65
 // to 96 have a form of 96, of which three blocks fit a compute unit: 6037 tokens in four
 // sequences, 12 heads of 80: 55 us, in the form of 128 67; 2 x 2048 tokens, 12 heads of
-// 80: 59 and 70. 64 rows a wave instead of 32 were slower: 2 x 8192 tokens, 16 heads of
-// 64: 808 us, with 32 690 (the exponentials of heads of 64 take as long as the products).
+// 80: 59 and 70. 64 rows a wave instead of 32 took 17% longer (2 x 8192 tokens, 16 heads of
+// 64, in turn: there the exponentials take as long as the products; 580 to 680 us now, by
+// the clock that the power limit leaves).
 template <class E, int D>
 __global__ __launch_bounds__(256, D == 96 ? 3 : 2) void k_attn_fwd(AttnK p, int tiles) {
   // Objects of their own, and turns of the loop that name theirs: the compiler then

@@ -15,9 +15,9 @@
 // them: the angles in 32 bits are twice a 16-bit row's bytes.
 //
 // Bound: HBM (each input read once, each output written once). 2 x 32768 tokens, 16 + 4
-// heads of 128, bf16: 150 us for 671 MB, 4.5 TB/s (a copy reaches 4.7). 3 x 5461 tokens,
-// 12 + 12 heads of 64: forward 24 us (101 MB), backward 33 (151 MB) and the weights'
-// partial sums 4.
+// heads of 128, bf16: 149 us for 671 MB in calls one after the other, 4.5 TB/s (a copy
+// reaches 4.7). 3 x 5461 tokens, 12 + 12 heads of 64: forward 24 us (101 MB), backward 33
+// (151 MB) and the weights' partial sums 4.
 #include "tokens_common.h"
 
 namespace {

@@ -6,8 +6,10 @@ through the rasterizer. The work runs in the HIP kernels behind the calls that
 shapes, allocate outputs and workspaces, and enqueue on the current stream (or
 ``stream``). They do no arithmetic of their own.
 
-Tensors are ``[batch, tokens, heads, dim]`` with any strides whose innermost is 1
-(views of a joint projection, say). The ``*_bwd`` functions take and return
+Tensors are ``[batch, tokens, heads, dim]`` by their strides (views of a joint
+projection, say): the elements of a head are contiguous, the tensor and its other
+strides are multiples of 16 bytes, and tokens are less than 2^23 elements apart; what
+does not fit is refused. The ``*_bwd`` functions take and return
 gradients explicitly; ``Attention``, ``QkNormRope`` and ``Dropout`` are the same
 calls for autograd (the first two have no second derivative: asking for it is an error).
 """
